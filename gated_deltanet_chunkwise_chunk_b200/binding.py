@@ -30,7 +30,9 @@ EXPORTED = ("gdn_workspace_bytes", "gdn_chunk_fwd", "gdn_chunk_bwd", "gdn_max_ch
             "gdn_recurrent_fwd", "gdn_recurrent_workspace_bytes", "gdn_kda_gate_fwd",
             "gdn_kda_gate_bwd", "gdn_kda_gate_workspace_bytes", "gdn_kda_recurrent_fwd",
             "gdn_kda_chunk_fwd", "gdn_kda_chunk_bwd", "gdn_kda_chunk_workspace_bytes",
-            "gdn_state_affine")
+            "gdn_state_affine", "gdn_conv_fwd", "gdn_conv_bwd", "gdn_conv_step", "gdn_conv_workspace_bytes",
+            "gdn_ssm_fwd", "gdn_ssm_bwd", "gdn_ssm_step", "gdn_ssm_workspace_bytes", "gdn_norm_fwd",
+            "gdn_norm_bwd", "gdn_norm_workspace_bytes")
 
 
 class gdn_dims(ctypes.Structure):
@@ -38,6 +40,21 @@ class gdn_dims(ctypes.Structure):
                 ("HV", ctypes.c_int64), ("K", ctypes.c_int64), ("V", ctypes.c_int64),
                 ("N", ctypes.c_int64), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("flags", ctypes.c_int32)]
+
+
+class gdn_conv_dims(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("B", "T", "D", "W", "N", "ld_x")] + [
+        ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class gdn_ssm_dims(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("B", "T", "D", "S", "G", "N", "ld_x", "ld_dt", "ld_b", "ld_c")] + [
+        ("dtype", ctypes.c_int32)]
+
+
+class gdn_norm_dims(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("rows", "D", "inner_x", "ld_x", "inner_gate", "ld_gate")] + [
+        ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class GDNError(RuntimeError):
@@ -79,6 +96,17 @@ def _load() -> ctypes.CDLL:
     lib.gdn_kda_gate_bwd.restype = I32
     lib.gdn_kda_gate_workspace_bytes.argtypes = [I64, I64, I64]
     lib.gdn_kda_gate_workspace_bytes.restype = SZ
+    CD, SD, ND = ctypes.POINTER(gdn_conv_dims), ctypes.POINTER(gdn_ssm_dims), ctypes.POINTER(gdn_norm_dims)
+    for name, args in (("gdn_conv_fwd", [CD] + [P] * 8 + [SZ, P]), ("gdn_conv_bwd", [CD] + [P] * 12 + [SZ, P]),
+                       ("gdn_conv_step", [CD] + [P] * 7), ("gdn_ssm_fwd", [SD] + [P] * 12 + [SZ, P]),
+                       ("gdn_ssm_bwd", [SD] + [P] * 19 + [SZ, P]), ("gdn_ssm_step", [SD] + [P] * 11),
+                       ("gdn_norm_fwd", [ND] + [P] * 7), ("gdn_norm_bwd", [ND] + [P] * 11 + [SZ, P])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = I32
+    for name, args in (("gdn_conv_workspace_bytes", [CD, I32, I32]), ("gdn_ssm_workspace_bytes", [SD, I32, I32]),
+                       ("gdn_norm_workspace_bytes", [ND])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = SZ
     lib.gdn_max_chunks.argtypes = [D, I32]
     lib.gdn_max_chunks.restype = I64
     lib.gdn_build_chunk_indices.argtypes = [D, P, P, I64]

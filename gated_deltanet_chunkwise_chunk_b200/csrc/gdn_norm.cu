@@ -1,0 +1,471 @@
+// Layer norm over the last axis, with optional weight, bias and gate; the rms form keeps the mean.
+//   xh = (x - mu) rstd,  n = xh w + b,  y = n  or  n silu(z)
+// Backward: dn = dy silu(z), dz = dy n silu'(z), u = dn w,
+//   dx = rstd (u - mean(u) - xh mean(u xh))   (rms: without mean(u)),
+//   dw = sum over rows of dn xh,  db = sum over rows of dn.
+// Bound by HBM: a row stays in registers between its statistics and its output, so x (z, dy) is read
+// once and y (dx, dz) written once.  A row belongs to a group of 1 to 32 lanes (up to 512 elements,
+// several rows to a block) or to a block of up to 512 threads; each thread holds NV vectors of it.  The variance
+// is the mean of (x - mu)^2 over the registers, not a difference of sums.  The backward's blocks walk
+// over many rows with the weight's and bias's sums in registers and the next row's loads in flight;
+// their partial rows are added in block order by a second kernel, so the sums do not depend on timing.
+#include <algorithm>
+
+#include "mix_common.cuh"
+
+namespace gdn {
+namespace mix {
+namespace {
+
+constexpr int NG = 256;  // threads of a block of lane groups
+
+template <int N>
+struct Vec {
+  float v[N];
+};
+
+// Sum of N values over the row's threads, the same result in each: lanes of the group by butterflies,
+// then the block's warps through shared memory in warp order.
+template <int N, bool BLOCK>
+__device__ __forceinline__ void row_sum(float (&a)[N], int lanes, float* sh) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (o >= lanes) continue;
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
+  }
+  if (BLOCK) {
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) sh[i * 32 + warp] = a[i];
+    }
+    __syncthreads();
+    const int l = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float v = l < warps ? sh[i * 32 + l] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      a[i] = v;
+    }
+  }
+}
+
+__device__ __forceinline__ int64_t row_at(int64_t r, int64_t inner, int64_t ld, int64_t D) {
+  if (inner == 1) return r * ld;
+  const int64_t o = r / inner;
+  return o * ld + (r - o * inner) * D;
+}
+
+// lanes: threads of a row; BLOCK: the whole block, else a power of two up to 32.
+template <typename T, int V, int NV, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? 512 : NG) k_norm_fwd(Norm c, int lanes) {
+  __shared__ float sh[2][2][32];
+  const int lane = BLOCK ? threadIdx.x : threadIdx.x & (lanes - 1);
+  const int rpb = BLOCK ? 1 : NG / lanes;
+  const int64_t step = (int64_t)gridDim.x * rpb;
+  const int64_t first = (int64_t)blockIdx.x * rpb + (BLOCK ? 0 : threadIdx.x / lanes);
+  const float inv = 1.f / (float)c.D;
+  const T* x = static_cast<const T*>(c.x);
+  const T* z = static_cast<const T*>(c.gate);
+  T* y = static_cast<T*>(c.y);
+  int col[NV];
+  bool live[NV];
+  float w[NV][V], b[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    col[i] = (i * lanes + lane) * V;
+    live[i] = col[i] < c.D;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      w[i][v] = live[i] && c.weight ? c.weight[col[i] + v] : 1.f;
+      b[i][v] = live[i] && c.bias ? c.bias[col[i] + v] : 0.f;
+    }
+  }
+  int flip = 0;
+  // every thread of a warp runs the same number of rounds (the butterflies need them all)
+  for (int64_t base = (int64_t)blockIdx.x * rpb, r = first; base < c.rows; base += step, r += step) {
+    const bool row = r < c.rows;
+    Pack<T, V> xr[NV], zr[NV];
+    const int64_t xa = row ? row_at(r, c.inner_x, c.ld_x, c.D) : 0;
+    const int64_t za = row && z ? row_at(r, c.inner_z, c.ld_z, c.D) : 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      xr[i].zero();
+      if (row && live[i]) {
+        xr[i].load_once(x + xa + col[i]);
+        if (z) zr[i].load_once(z + za + col[i]);
+      }
+    }
+    float mu = 0.f;
+    if (!c.rms) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[0] += up<T>(xr[i].v[v]);
+      row_sum<1, BLOCK>(s, lanes, sh[flip][0]);
+      mu = s[0] * inv;
+    }
+    float q[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float d = up<T>(xr[i].v[v]) - mu;
+        if (live[i]) q[0] = fmaf(d, d, q[0]);
+      }
+    row_sum<1, BLOCK>(q, lanes, sh[flip][1]);
+    flip ^= 1;
+    const float rstd = rsqrtf(fmaf(q[0], inv, c.eps));
+    if (!row) continue;
+    if (c.stats && lane == 0) {
+      c.stats[2 * r] = mu;
+      c.stats[2 * r + 1] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!live[i]) continue;
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        o[v] = fmaf((up<T>(xr[i].v[v]) - mu) * rstd, w[i][v], b[i][v]);
+        if (z) {
+          const float g = up<T>(zr[i].v[v]);
+          o[v] *= g * sigmoid<T>(g);
+        }
+      }
+      Pack<T, V> out;
+      out.set(o);
+      out.store(y + r * c.D + col[i]);
+    }
+  }
+}
+
+template <typename T, int V, int NV, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? 512 : NG) k_norm_bwd(Norm c, int lanes) {
+  __shared__ float sh[2][2][32];
+  __shared__ float red[BLOCK ? 1 : NG * V];
+  const int lane = BLOCK ? threadIdx.x : threadIdx.x & (lanes - 1);
+  const int rpb = BLOCK ? 1 : NG / lanes;
+  const int64_t step = (int64_t)gridDim.x * rpb;
+  const float inv = 1.f / (float)c.D;
+  const T* x = static_cast<const T*>(c.x);
+  const T* z = static_cast<const T*>(c.gate);
+  const T* dy = static_cast<const T*>(c.dy);
+  int col[NV];
+  bool live[NV];
+  float w[NV][V], b[NV][V], dw[NV][V], db[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    col[i] = (i * lanes + lane) * V;
+    live[i] = col[i] < c.D;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      w[i][v] = live[i] && c.weight ? c.weight[col[i] + v] : 1.f;
+      b[i][v] = live[i] && c.bias && z ? c.bias[col[i] + v] : 0.f;
+      dw[i][v] = db[i][v] = 0.f;
+    }
+  }
+  Pack<T, V> xr[NV], zr[NV], gr[NV];
+  float mu = 0.f, rstd = 0.f;
+  auto fetch = [&](int64_t r) {
+    const bool row = r < c.rows;
+    const int64_t xa = row ? row_at(r, c.inner_x, c.ld_x, c.D) : 0;
+    const int64_t za = row && z ? row_at(r, c.inner_z, c.ld_z, c.D) : 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      xr[i].zero();
+      gr[i].zero();
+      zr[i].zero();
+      if (row && live[i]) {
+        xr[i].load_once(x + xa + col[i]);
+        gr[i].load_once(dy + r * c.D + col[i]);
+        if (z) zr[i].load_once(z + za + col[i]);
+      }
+    }
+    mu = row ? c.stats[2 * r] : 0.f;
+    rstd = row ? c.stats[2 * r + 1] : 0.f;
+  };
+  int64_t r = (int64_t)blockIdx.x * rpb + (BLOCK ? 0 : threadIdx.x / lanes);
+  if ((int64_t)blockIdx.x * rpb < c.rows) fetch(r);
+  int flip = 0;
+  for (int64_t base = (int64_t)blockIdx.x * rpb; base < c.rows; base += step, r += step) {
+    const bool row = r < c.rows;
+    const float m = mu, rs = rstd;
+    float xh[NV][V], u[NV][V];
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float dz[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float h = live[i] ? (up<T>(xr[i].v[v]) - m) * rs : 0.f;
+        float dn = up<T>(gr[i].v[v]);
+        if (z) {
+          const float g = up<T>(zr[i].v[v]), sg = sigmoid<T>(g), n = fmaf(h, w[i][v], b[i][v]);
+          dz[v] = dn * n * sg * fmaf(g, 1.f - sg, 1.f);
+          dn *= g * sg;
+        }
+        if (row && live[i]) {
+          dw[i][v] = fmaf(dn, h, dw[i][v]);
+          db[i][v] += dn;
+        }
+        xh[i][v] = h;
+        u[i][v] = dn * w[i][v];
+        s[0] += u[i][v];
+        s[1] = fmaf(u[i][v], h, s[1]);
+      }
+      if (z && row && live[i]) {
+        Pack<T, V> out;
+        out.set(dz);
+        out.store(static_cast<T*>(c.dgate) + r * c.D + col[i]);
+      }
+    }
+    fetch(r + step);
+    row_sum<2, BLOCK>(s, lanes, sh[flip][0]);
+    flip ^= 1;
+    if (!row) continue;
+    const float a0 = c.rms ? 0.f : s[0] * inv, a1 = s[1] * inv;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!live[i]) continue;
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[v] = rs * (u[i][v] - a0 - xh[i][v] * a1);
+      Pack<T, V> out;
+      out.set(o);
+      out.store(static_cast<T*>(c.dx) + r * c.D + col[i]);
+    }
+  }
+  if (!c.part) return;
+  float* part = c.part + (int64_t)blockIdx.x * (c.dbias ? 2 : 1) * c.D;
+  if constexpr (BLOCK) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (live[i]) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          part[col[i] + v] = dw[i][v];
+          if (c.dbias) part[c.D + col[i] + v] = db[i][v];
+        }
+      }
+  } else {
+    for (int k = 0; k < (c.dbias ? 2 : 1); ++k)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; ++v) red[threadIdx.x * V + v] = k ? db[i][v] : dw[i][v];
+        __syncthreads();
+        if ((int)threadIdx.x < lanes && live[i]) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            float a = 0.f;
+            for (int g = 0; g < rpb; ++g) a += red[(g * lanes + lane) * V + v];
+            part[k * c.D + col[i] + v] = a;
+          }
+        }
+      }
+  }
+}
+
+// Rows too wide for the registers of a block: the same in three passes over the row, which the
+// caches hold.  The sums of the block's rows stay in its partial row in memory.
+template <typename T>
+__global__ void __launch_bounds__(1024) k_norm_fwd_wide(Norm c) {
+  __shared__ float sh[2][32];
+  for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
+    const T* x = static_cast<const T*>(c.x) + row_at(r, c.inner_x, c.ld_x, c.D);
+    const T* z = c.gate ? static_cast<const T*>(c.gate) + row_at(r, c.inner_z, c.ld_z, c.D) : nullptr;
+    const float inv = 1.f / (float)c.D;
+    float mu = 0.f;
+    if (!c.rms) {
+      float s[1] = {0.f};
+      for (int64_t i = threadIdx.x; i < c.D; i += blockDim.x) s[0] += up<T>(x[i]);
+      row_sum<1, true>(s, 32, sh[0]);
+      mu = s[0] * inv;
+    }
+    float q[1] = {0.f};
+    for (int64_t i = threadIdx.x; i < c.D; i += blockDim.x) {
+      const float d = up<T>(x[i]) - mu;
+      q[0] = fmaf(d, d, q[0]);
+    }
+    row_sum<1, true>(q, 32, sh[1]);
+    const float rstd = rsqrtf(fmaf(q[0], inv, c.eps));
+    if (c.stats && threadIdx.x == 0) {
+      c.stats[2 * r] = mu;
+      c.stats[2 * r + 1] = rstd;
+    }
+    for (int64_t i = threadIdx.x; i < c.D; i += blockDim.x) {
+      float o = fmaf((up<T>(x[i]) - mu) * rstd, c.weight ? c.weight[i] : 1.f, c.bias ? c.bias[i] : 0.f);
+      if (z) {
+        const float g = up<T>(z[i]);
+        o *= g * sigmoid<T>(g);
+      }
+      static_cast<T*>(c.y)[r * c.D + i] = down<T>(o);
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(1024) k_norm_bwd_wide(Norm c) {
+  __shared__ float sh[2][32];
+  const int parts = c.dbias ? 2 : 1;
+  float* part = c.part ? c.part + (int64_t)blockIdx.x * parts * c.D : nullptr;
+  bool first = true;
+  for (int64_t r = blockIdx.x; r < c.rows; r += gridDim.x) {
+    const T* x = static_cast<const T*>(c.x) + row_at(r, c.inner_x, c.ld_x, c.D);
+    const T* z = c.gate ? static_cast<const T*>(c.gate) + row_at(r, c.inner_z, c.ld_z, c.D) : nullptr;
+    const T* dy = static_cast<const T*>(c.dy) + r * c.D;
+    const float mu = c.stats[2 * r], rs = c.stats[2 * r + 1], inv = 1.f / (float)c.D;
+    float s[2] = {0.f, 0.f};
+    for (int64_t i = threadIdx.x; i < c.D; i += blockDim.x) {
+      const float h = (up<T>(x[i]) - mu) * rs, w = c.weight ? c.weight[i] : 1.f;
+      float dn = up<T>(dy[i]);
+      if (z) {
+        const float g = up<T>(z[i]), sg = sigmoid<T>(g), n = fmaf(h, w, c.bias ? c.bias[i] : 0.f);
+        static_cast<T*>(c.dgate)[r * c.D + i] = down<T>(dn * n * sg * fmaf(g, 1.f - sg, 1.f));
+        dn *= g * sg;
+      }
+      if (part) {
+        part[i] = first ? dn * h : fmaf(dn, h, part[i]);
+        if (c.dbias) part[c.D + i] = first ? dn : part[c.D + i] + dn;
+      }
+      s[0] = fmaf(dn, w, s[0]);
+      s[1] = fmaf(dn * w, h, s[1]);
+    }
+    first = false;
+    row_sum<2, true>(s, 32, sh[0]);
+    const float a0 = c.rms ? 0.f : s[0] * inv, a1 = s[1] * inv;
+    for (int64_t i = threadIdx.x; i < c.D; i += blockDim.x) {
+      const float h = (up<T>(x[i]) - mu) * rs;
+      float dn = up<T>(dy[i]);
+      if (z) {
+        const float g = up<T>(z[i]);
+        dn *= g * sigmoid<T>(g);
+      }
+      static_cast<T*>(c.dx)[r * c.D + i] = down<T>(rs * (dn * (c.weight ? c.weight[i] : 1.f) - a0 - h * a1));
+    }
+    __syncthreads();
+  }
+}
+
+bool vec_ok(const Norm& c, int es) {
+  const int V = 16 / es;
+  if (c.D % V || c.ld_x % V || (c.gate && c.ld_z % V)) return false;
+  const void* ps[] = {c.x, c.gate, c.y, c.dy, c.dx, c.dgate};
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) % 16) return false;
+  return true;
+}
+
+// How a call is launched; a function of the sizes and the vector width only.
+struct Plan {
+  bool wide, block;
+  int nv, threads;  // vectors of a thread; threads of a row
+  int64_t blocks;
+};
+
+// The backward's blocks walk over rows: four resident blocks of 256 threads on each of 148
+// multiprocessors, or two of 512.
+constexpr int64_t kBwdBlocks = 592;
+
+Plan make_plan(int64_t rows, int64_t D, int V, bool bwd) {
+  Plan p{};
+  const int64_t vecs = (D + V - 1) / V;
+  const int most = (bwd ? 16 : 32) / V;  // elements of a row that a thread may hold, in vectors
+  p.wide = vecs > 512 * (int64_t)most;
+  p.block = D > 512;
+  p.nv = 1;
+  if (p.wide) {
+    p.threads = 1024;
+    p.blocks = std::min(rows, bwd ? kBwdBlocks / 2 : (int64_t)148 * 2);
+    return p;
+  }
+  if (p.block) {
+    while ((vecs + p.nv - 1) / p.nv > 512) p.nv *= 2;
+    p.threads = (int)(((vecs + p.nv - 1) / p.nv + 31) / 32 * 32);
+    p.blocks = std::min<int64_t>(rows, bwd ? kBwdBlocks * 256 / std::max(256, p.threads) : 148 * (2048 / p.threads));
+    return p;
+  }
+  while ((vecs + p.nv - 1) / p.nv > 32) p.nv *= 2;
+  p.threads = 1;
+  while ((int64_t)p.threads * p.nv < vecs) p.threads *= 2;
+  const int rpb = NG / p.threads;
+  p.blocks = std::min((rows + rpb - 1) / rpb, bwd ? kBwdBlocks : (int64_t)148 * 8);
+  return p;
+}
+
+template <typename T, int V, int NV, bool BWD>
+cudaError_t launch_nv(const Norm& c, const Plan& p, cudaStream_t s) {
+  if constexpr (V * NV <= (BWD ? 16 : 32)) {
+    const unsigned n = (unsigned)p.blocks;
+    if constexpr (BWD)
+      p.block ? k_norm_bwd<T, V, NV, true><<<n, p.threads, 0, s>>>(c, p.threads)
+              : k_norm_bwd<T, V, NV, false><<<n, NG, 0, s>>>(c, p.threads);
+    else
+      p.block ? k_norm_fwd<T, V, NV, true><<<n, p.threads, 0, s>>>(c, p.threads)
+              : k_norm_fwd<T, V, NV, false><<<n, NG, 0, s>>>(c, p.threads);
+    return cudaGetLastError();
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename T, int V, bool BWD>
+cudaError_t launch(const Norm& c, cudaStream_t s, int64_t* blocks) {
+  const Plan p = make_plan(c.rows, c.D, V, BWD);
+  *blocks = p.blocks;
+  if (p.wide) {
+    if constexpr (BWD)
+      k_norm_bwd_wide<T><<<(unsigned)p.blocks, p.threads, 0, s>>>(c);
+    else
+      k_norm_fwd_wide<T><<<(unsigned)p.blocks, p.threads, 0, s>>>(c);
+    return cudaGetLastError();
+  }
+  switch (p.nv) {
+    case 1: return launch_nv<T, V, 1, BWD>(c, p, s);
+    case 2: return launch_nv<T, V, 2, BWD>(c, p, s);
+    case 4: return launch_nv<T, V, 4, BWD>(c, p, s);
+    case 8: return launch_nv<T, V, 8, BWD>(c, p, s);
+    case 16: return launch_nv<T, V, 16, BWD>(c, p, s);
+    default: return launch_nv<T, V, 32, BWD>(c, p, s);
+  }
+}
+
+template <bool BWD>
+cudaError_t dispatch(const Norm& c, cudaStream_t s, int64_t* n) {
+  if (c.dtype == GDN_DTYPE_FP32) return vec_ok(c, 4) ? launch<float, 4, BWD>(c, s, n) : launch<float, 1, BWD>(c, s, n);
+  const bool v = vec_ok(c, 2);
+  if (c.dtype == GDN_DTYPE_BF16)
+    return v ? launch<__nv_bfloat16, 8, BWD>(c, s, n) : launch<__nv_bfloat16, 1, BWD>(c, s, n);
+  return v ? launch<__half, 8, BWD>(c, s, n) : launch<__half, 1, BWD>(c, s, n);
+}
+
+}  // namespace
+
+size_t norm_bwd_part_floats(int64_t rows, int64_t D) { return (size_t)std::min(rows, kBwdBlocks) * 2 * D; }
+
+cudaError_t norm_forward(const Norm& c, cudaStream_t s) {
+  if (c.rows == 0) return cudaSuccess;
+  ProfScope ps("norm_fwd", s);
+  int64_t blocks = 0;
+  return dispatch<false>(c, s, &blocks);
+}
+
+cudaError_t norm_backward(const Norm& c, cudaStream_t s) {
+  int64_t blocks = 0;
+  if (c.rows > 0) {
+    ProfScope ps("norm_bwd", s);
+    const cudaError_t e = dispatch<true>(c, s, &blocks);
+    if (e != cudaSuccess) return e;
+  }
+  if (!c.dweight && !c.dbias) return cudaSuccess;
+  return column_sums("norm_bwd_sums", c.part, blocks, (c.dbias ? 2 : 1) * c.D, (c.dbias ? 2 : 1) * c.D, c.dweight, c.dbias,
+                     1, c.D, s);
+}
+
+}  // namespace mix
+}  // namespace gdn

@@ -68,7 +68,7 @@ typedef enum gdn_status {
 typedef enum gdn_dtype {
   GDN_DTYPE_FP32 = 0,
   GDN_DTYPE_BF16 = 1,
-  GDN_DTYPE_FP16 = 2  /* the KDA gate entry points only */
+  GDN_DTYPE_FP16 = 2  /* the KDA gate and the mixing-layer entry points only */
 } gdn_dtype;
 
 typedef struct gdn_dims {
@@ -270,6 +270,122 @@ size_t gdn_kda_gate_workspace_bytes(int64_t T, int64_t H, int64_t D);
  * 1 <= K <= 128, V a multiple of 32; GDN_ERR_INVALID_ARG otherwise. */
 int gdn_state_affine(int64_t count, int64_t K, int64_t V, const float* A, int transpose_a, const float* X,
                      const float* B, float* out, void* stream);
+
+/* ---- Mixing-layer operators: what a layer runs before and after its recurrence ----------------
+ *
+ * Common to the entry points below.  Tensors with a token stride (ld_*, in elements; 0 = contiguous)
+ * may be slices of a wider projection: token t of sequence b starts at element (b T + t) ld, and its
+ * row is contiguous; such inputs need element alignment only (rows whose width, stride and base are
+ * multiples of 16 bytes move in 16-byte accesses).  All other buffers are contiguous with 16-byte
+ * aligned bases.  dtype: fp32, bf16 or fp16 for every per-token tensor of a call (and the
+ * convolution's states); parameters, scan states and parameter gradients are fp32; all arithmetic
+ * and all sums are fp32 and deterministic (no atomics).  Outputs must not overlap inputs
+ * (GDN_ERR_INVALID_ARG), except a step's final_state, which may be its state.
+ * Varlen as above: cu_seqlens packs N sequences into batch row 0, B = 1, cu[N] = T; empty sequences
+ * pass their state through.  Invalid values set the workspace's status word and nothing is written.
+ * Limits (GDN_ERR_INVALID_ARG): B T <= 2^30 tokens, widths <= 2^20. */
+
+typedef struct gdn_conv_dims {
+  int64_t B, T, D, W;  /* D channels, W taps (1..8, else GDN_ERR_UNSUPPORTED) */
+  int64_t N;           /* packed sequences when cu_seqlens != NULL; ignored otherwise */
+  int64_t ld_x;        /* token stride of x */
+  int32_t dtype;
+  int32_t flags;       /* gdn_conv_flags */
+} gdn_conv_dims;
+
+typedef enum gdn_conv_flags { GDN_CONV_SILU = 1 /* y = silu(pre) instead of pre */ } gdn_conv_flags;
+
+/* Short causal convolution of each channel along the sequence:
+ *   pre[t,d] = bias[d] + sum_{j<W} weight[d,j] x[t-(W-1)+j, d],   y = silu(pre) or pre.
+ * x, y [B,T,D]; weight [D,W]; bias [D] or NULL; states [Nst, W-1, D] in dtype, the sequence's last
+ * W - 1 inputs, oldest first.  initial_state NULL = zeros; final_state NULL = not written.
+ * workspace: gdn_conv_workspace_bytes(d, varlen, 0), 256-byte aligned (the status word). */
+int gdn_conv_fwd(const gdn_conv_dims* d, const void* x, const float* weight, const float* bias,
+                 const int64_t* cu_seqlens, const void* initial_state, void* y, void* final_state,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward of L = sum(dy * y) + sum(dfinal_state * final_state), from the forward's inputs (pre is
+ * recomputed).  dx [B,T,D] contiguous; dweight [D,W], dbias [D], dinitial_state may be NULL
+ * (skipped); dfinal_state may be NULL (zero).  workspace: gdn_conv_workspace_bytes(d, varlen, 1). */
+int gdn_conv_bwd(const gdn_conv_dims* d, const void* x, const float* weight, const float* bias,
+                 const int64_t* cu_seqlens, const void* initial_state, const void* dy,
+                 const void* dfinal_state, void* dx, float* dweight, float* dbias,
+                 void* dinitial_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token for each of B sequences (T = 1): x, y [B,D]; state and final_state [B, W-1, D], which may
+ * be the same buffer (updated in place; both may be NULL when W = 1). */
+int gdn_conv_step(const gdn_conv_dims* d, const void* x, const float* weight, const float* bias,
+                  const void* state, void* y, void* final_state, void* stream);
+
+size_t gdn_conv_workspace_bytes(const gdn_conv_dims* d, int varlen, int pass);
+
+typedef struct gdn_ssm_dims {
+  int64_t B, T, D, S, G;  /* D channels of S states each (S <= 64, else GDN_ERR_UNSUPPORTED), G groups */
+  int64_t N;              /* packed sequences when cu_seqlens != NULL; ignored otherwise */
+  int64_t ld_x, ld_dt, ld_b, ld_c;  /* token strides of x, dt, Bm, Cm */
+  int32_t dtype;
+} gdn_ssm_dims;
+
+/* Selective state space scan (a decay per channel and state, input-dependent step, B and C):
+ *   delta = softplus(dt + dt_bias[d]) (x > 20 passes through),  A = -exp(A_log[d,s]),
+ *   h[t,d,s] = exp(delta A) h[t-1,d,s] + delta x[t,d] Bm[t,g,s],
+ *   y[t,d] = sum_s Cm[t,g,s] h[t,d,s] + D_skip[d] x[t,d],      g = d / (D / G).
+ * x, dt, y [B,T,D]; Bm, Cm [B,T,G,S] (a token's G S values contiguous); A_log [D,S]; D_skip and dt_bias
+ * [D] or NULL (none); states [Nst, D, S] fp32.  initial_state NULL = zeros; final_state NULL = not
+ * written.  For prompts of any length; gdn_ssm_step decodes.  workspace: gdn_ssm_workspace_bytes(d,
+ * varlen, 0) bytes, 256-byte aligned; given at least the bytes of pass 1, the forward also keeps in it
+ * the states that gdn_ssm_bwd reads (one in 16 tokens). */
+int gdn_ssm_fwd(const gdn_ssm_dims* d, const void* x, const void* dt, const float* A_log,
+                const void* Bm, const void* Cm, const float* D_skip, const float* dt_bias,
+                const int64_t* cu_seqlens, const float* initial_state, void* y, float* final_state,
+                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward of L = sum(dy * y) + sum(dfinal_state * final_state).  `workspace` is the one (pass 1) in
+ * which gdn_ssm_fwd kept the states for the same inputs; it may be read by several backward calls,
+ * one after the other.  dx, ddt [B,T,D], dB, dC [B,T,G,S] contiguous, in dtype; dA_log [D,S],
+ * dD_skip [D], ddt_bias [D], dinitial_state [Nst,D,S] fp32, each may be NULL (skipped).
+ * dfinal_state NULL = zero. */
+int gdn_ssm_bwd(const gdn_ssm_dims* d, const void* x, const void* dt, const float* A_log,
+                const void* Bm, const void* Cm, const float* D_skip, const float* dt_bias,
+                const int64_t* cu_seqlens, const void* dy, const float* dfinal_state, void* dx,
+                void* ddt, void* dB, void* dC, float* dA_log, float* dD_skip, float* ddt_bias,
+                float* dinitial_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token for each of B sequences (T = 1): x, dt, y [B,D]; Bm, Cm [B,G,S]; state and final_state
+ * [B,D,S], which may be the same buffer (updated in place). */
+int gdn_ssm_step(const gdn_ssm_dims* d, const void* x, const void* dt, const float* A_log,
+                 const void* Bm, const void* Cm, const float* D_skip, const float* dt_bias,
+                 const float* state, void* y, float* final_state, void* stream);
+
+size_t gdn_ssm_workspace_bytes(const gdn_ssm_dims* d, int varlen, int pass);
+
+typedef struct gdn_norm_dims {
+  int64_t rows, D;
+  int64_t inner_x, ld_x;        /* row r of x starts at (r / inner_x) ld_x + (r % inner_x) D: */
+  int64_t inner_gate, ld_gate;  /* the heads of a token's slice; 0, 0 = contiguous rows */
+  int32_t dtype;
+  int32_t flags;                /* gdn_norm_flags */
+  float eps;                    /* >= 0 */
+} gdn_norm_dims;
+
+typedef enum gdn_norm_flags { GDN_NORM_RMS = 1 /* keep the mean */ } gdn_norm_flags;
+
+/* Layer norm over rows of D elements, as a block's norm or as the gated norm of a recurrence's heads:
+ *   mu = mean(x) (0 with GDN_NORM_RMS),  rstd = 1 / sqrt(mean((x - mu)^2) + eps),
+ *   y = n or, with a gate, n silu(gate),   n = (x - mu) rstd weight + bias.
+ * weight, bias [D] or NULL; gate like x or NULL; y [rows,D] contiguous; stats [rows,2] fp32 (mu, rstd)
+ * or NULL: what gdn_norm_bwd reads. */
+int gdn_norm_fwd(const gdn_norm_dims* d, const void* x, const float* weight, const float* bias,
+                 const void* gate, void* y, float* stats, void* stream);
+
+/* Backward for dy [rows,D]: dx, dgate (exactly when there is a gate) [rows,D] contiguous in dtype;
+ * dweight, dbias [D] fp32, each may be NULL (skipped).  workspace: gdn_norm_workspace_bytes(d),
+ * 256-byte aligned; not needed when both are NULL. */
+int gdn_norm_bwd(const gdn_norm_dims* d, const void* x, const float* weight, const float* bias,
+                 const void* gate, const float* stats, const void* dy, void* dx, void* dgate,
+                 float* dweight, float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+size_t gdn_norm_workspace_bytes(const gdn_norm_dims* d);
 
 /* Upper bound on the number of 64-token chunks (the grid size used for chunk kernels). */
 int64_t gdn_max_chunks(const gdn_dims* d, int varlen);
