@@ -31,39 +31,30 @@ cudaError_t check_packing(const Seqs& s, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// 32 columns x 32 strands of rows; each strand in row order, the strands in a fixed tree.
-__global__ void __launch_bounds__(1024) k_column_sums(const float* __restrict__ part, int64_t n, int64_t ld,
-                                                      int64_t width, float* __restrict__ out,
-                                                      float* __restrict__ out2, int W, int64_t D) {
-  __shared__ float red[32][33];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + tx;
-  float a = 0.f;
-  if (c < width)
-    for (int64_t r = ty; r < n; r += 32) a += part[r * ld + c];
-  red[ty][tx] = a;
-  __syncthreads();
-  float v = red[tx][ty];  // strand tx of column ty
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int64_t cc = (int64_t)blockIdx.x * 32 + ty;
-  if (tx != 0 || cc >= width) return;
-  if (W == 0) {
-    out[cc] = v;
-  } else {
-    const int64_t j = cc / D, d = cc - j * D;
-    if (j < W) {
-      if (out) out[d * W + j] = v;
-    } else if (out2) {
-      out2[d] = v;
-    }
+// Columns x STR strands of rows; each strand in row order, the strands in a fixed tree.
+template <int STR>
+__global__ void __launch_bounds__(STR == 1 ? 256 : 32 * STR) k_column_sums(const float* __restrict__ part, int64_t n, int64_t ld,
+                                                                          int64_t width, float* __restrict__ out,
+                                                                          float* __restrict__ out2, int W, int64_t D) {
+  int64_t c;
+  const float v = strand_sums<STR>(part, n, ld, width, c);
+  if (c < 0) return;
+  const int64_t j = c / D, d = c - j * D;
+  if (j < W) {
+    if (out) out[d * W + j] = v;
+  } else if (out2) {
+    out2[d] = v;
   }
 }
 
 cudaError_t column_sums(const char* name, const float* part, int64_t n, int64_t ld, int64_t width, float* out,
                         float* out2, int W, int64_t D, cudaStream_t s) {
   ProfScope ps(name, s);
-  k_column_sums<<<(unsigned)((width + 31) / 32), 1024, 0, s>>>(part, n, ld, width, out, out2, W, D);
+  switch (sum_strands(n)) {
+    case 1: k_column_sums<1><<<(unsigned)((width + 255) / 256), 256, 0, s>>>(part, n, ld, width, out, out2, W, D); break;
+    case 8: k_column_sums<8><<<(unsigned)((width + 31) / 32), 256, 0, s>>>(part, n, ld, width, out, out2, W, D); break;
+    default: k_column_sums<32><<<(unsigned)((width + 31) / 32), 1024, 0, s>>>(part, n, ld, width, out, out2, W, D);
+  }
   return cudaGetLastError();
 }
 

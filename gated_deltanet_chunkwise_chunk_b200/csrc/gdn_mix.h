@@ -78,9 +78,10 @@ struct Ssm {
   Seqs seqs;
   int64_t D, ld_x, ld_dt, ld_b, ld_c;
   int N, G, dtype;
-  int lg;    // log2 of a segment's tokens
+  int lg;    // log2 of a segment's tokens, in the direction that runs
   bool cut;  // whether a sequence may have several segments
-  bool vec;  // whether the per-channel tensors take vector accesses
+  bool vec;     // whether the per-channel tensors take 16-byte accesses
+  bool vec_bc;  // whether B and C do
   const void* x;
   const void* dt;
   const float* A_log;
@@ -112,8 +113,8 @@ struct Ssm {
 
 // What a call needs besides the status word; offsets are the caller's.
 struct SsmSizes {
-  int lg;
-  bool cut;
+  int lg[2];    // forward, backward
+  bool cut[2];
   int64_t starts, sums, ckpt, part_bc, part_par;  // floats
 };
 int ssm_padded(int N);
@@ -122,8 +123,11 @@ cudaError_t ssm_forward(const Ssm& c, cudaStream_t s);
 cudaError_t ssm_backward(const Ssm& c, cudaStream_t s);
 cudaError_t ssm_step(const Ssm& c, cudaStream_t s);
 
-// Column sums of partial rows part[r * ld + c], r < n, in a fixed order.  W = 0: out[c] for c < width.
-// W > 0 (the convolution's rows [W + 1][D]): column j D + d goes to out[d W + j], the last D to out2.
+// Strands of rows that a sum of n partial rows is split into, by n alone.
+inline int sum_strands(int64_t n) { return n <= 8 ? 1 : n <= 128 ? 8 : 32; }
+
+// Column sums of partial rows part[r * ld + c], r < n, in a fixed order: column j D + d of a row [W + 1][D] goes
+// to out[d W + j], the last D to out2; either may be null.
 cudaError_t column_sums(const char* name, const float* part, int64_t n, int64_t ld, int64_t width, float* out,
                         float* out2, int W, int64_t D, cudaStream_t s);
 

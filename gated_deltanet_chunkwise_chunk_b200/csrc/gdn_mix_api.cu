@@ -129,7 +129,7 @@ SsmPlan ssm_plan(const gdn_ssm_dims* d, bool varlen) {
   return p;
 }
 
-Ssm ssm_of(const gdn_ssm_dims* d, const Seqs& s, const SsmPlan& p, void* ws) {
+Ssm ssm_of(const gdn_ssm_dims* d, const Seqs& s, const SsmPlan& p, void* ws, int pass) {
   Ssm c{};
   c.seqs = s;
   c.D = d->D;
@@ -140,8 +140,8 @@ Ssm ssm_of(const gdn_ssm_dims* d, const Seqs& s, const SsmPlan& p, void* ws) {
   c.ld_dt = d->ld_dt ? d->ld_dt : d->D;
   c.ld_b = d->ld_b ? d->ld_b : d->G * d->S;
   c.ld_c = d->ld_c ? d->ld_c : d->G * d->S;
-  c.lg = p.z.lg;
-  c.cut = p.z.cut;
+  c.lg = p.z.lg[pass];
+  c.cut = p.z.cut[pass];
   char* b = static_cast<char*>(ws);
   auto at = [&](size_t o) { return reinterpret_cast<float*>(b + o); };
   c.starts = at(p.starts);
@@ -152,14 +152,19 @@ Ssm ssm_of(const gdn_ssm_dims* d, const Seqs& s, const SsmPlan& p, void* ws) {
   return c;
 }
 
-// Vector accesses of x, dt, y (dy, dx, ddt): a warp's channels are whole and their rows aligned.
+// 16-byte accesses of x, dt, y (dy, dx, ddt): rows, their strides and a group's channels are multiples.
 bool ssm_vec(const Ssm& c) {
-  const int CW = 128 / ssm_padded(c.N);
-  const size_t es = esize(c.dtype), b = CW * es > 16 ? 16 : CW * es;
-  const int V = (int)(b / es);
-  if ((c.D / c.G) % CW || c.ld_x % V || c.ld_dt % V || c.D % V) return false;
+  const int V = (int)(16 / esize(c.dtype));
+  if ((c.D / c.G) % V || c.ld_x % V || c.ld_dt % V) return false;
   const void* ps[] = {c.x, c.dt, c.y, c.dy, c.dx, c.ddt};
-  return !any_misaligned(ps, b);
+  return !any_misaligned(ps, 16);
+}
+// and of B and C
+bool ssm_vec_bc(const Ssm& c) {
+  const int V = (int)(16 / esize(c.dtype));
+  if (c.N % V || c.ld_b % V || c.ld_c % V) return false;
+  const void* ps[] = {c.Bm, c.Cm};
+  return !any_misaligned(ps, 16);
 }
 
 // ------------------------------------------------------------------------------ norm
@@ -305,7 +310,7 @@ int gdn_ssm_fwd(const gdn_ssm_dims* d, const void* x, const void* dt, const floa
   if (any_misaligned(el, es) || any_misaligned(ps, 16)) return GDN_ERR_INVALID_ARG;
   const SsmPlan p = ssm_plan(d, varlen);
   if (!workspace_ok(workspace, workspace_bytes, p.fwd)) return GDN_ERR_WORKSPACE;
-  Ssm c = ssm_of(d, sequences(d->B, d->T, d->N, cu_seqlens, varlen, workspace), p, workspace);
+  Ssm c = ssm_of(d, sequences(d->B, d->T, d->N, cu_seqlens, varlen, workspace), p, workspace, 0);
   const size_t rows = (size_t)R * d->D * es;
   if (overlap(initial_state, st, final_state, st) || overlap(x, extent(R, c.ld_x, d->D, es), y, rows) ||
       overlap(dt, extent(R, c.ld_dt, d->D, es), y, rows) || overlap(Bm, extent(R, c.ld_b, d->G * d->S, es), y, rows) ||
@@ -323,6 +328,7 @@ int gdn_ssm_fwd(const gdn_ssm_dims* d, const void* x, const void* dt, const floa
   c.final = final_state;
   if (workspace_bytes < p.total) c.ckpt = nullptr;
   c.vec = ssm_vec(c);
+  c.vec_bc = ssm_vec_bc(c);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (varlen)
     if (cudaError_t e = check_packing(c.seqs, s)) return status_of(e);
@@ -344,7 +350,7 @@ int gdn_ssm_bwd(const gdn_ssm_dims* d, const void* x, const void* dt, const floa
   if (any_misaligned(el, es) || any_misaligned(ps, 16)) return GDN_ERR_INVALID_ARG;
   const SsmPlan p = ssm_plan(d, varlen);
   if (!workspace_ok(workspace, workspace_bytes, p.total)) return GDN_ERR_WORKSPACE;
-  Ssm c = ssm_of(d, sequences(d->B, d->T, d->N, cu_seqlens, varlen, workspace), p, workspace);
+  Ssm c = ssm_of(d, sequences(d->B, d->T, d->N, cu_seqlens, varlen, workspace), p, workspace, 1);
   const size_t rows = (size_t)R * d->D * es, mats = (size_t)R * d->G * d->S * es;
   const void* outs[] = {dx, ddt, dB, dC};
   const size_t outn[] = {rows, rows, mats, mats};
@@ -376,6 +382,7 @@ int gdn_ssm_bwd(const gdn_ssm_dims* d, const void* x, const void* dt, const floa
   c.ddt_bias = ddt_bias;
   c.dinit = dinitial_state;
   c.vec = ssm_vec(c);
+  c.vec_bc = ssm_vec_bc(c);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (varlen)
     if (cudaError_t e = check_packing(c.seqs, s)) return status_of(e);
@@ -393,7 +400,7 @@ int gdn_ssm_step(const gdn_ssm_dims* d, const void* x, const void* dt, const flo
   const void* el[] = {x, dt, Bm, Cm};
   const void* ps[] = {A_log, D_skip, dt_bias, state, y, final_state};
   if (any_misaligned(el, es) || any_misaligned(ps, 16)) return GDN_ERR_INVALID_ARG;
-  Ssm c = ssm_of(d, sequences(d->B, 1, 0, nullptr, false, nullptr), SsmPlan{}, nullptr);
+  Ssm c = ssm_of(d, sequences(d->B, 1, 0, nullptr, false, nullptr), SsmPlan{}, nullptr, 0);
   const size_t rows = (size_t)d->B * d->D * es;
   if ((state != final_state && overlap(state, st, final_state, st)) || overlap(x, extent(d->B, c.ld_x, d->D, es), y, rows) ||
       overlap(dt, extent(d->B, c.ld_dt, d->D, es), y, rows))

@@ -5,10 +5,14 @@
 //   dA_log = A sum_t delta q,  dDskip = sum_t dy x,  ddt_bias = sum_t ddt.
 // The states come from the forward's every-16th-token copies: a warp goes through 16 tokens forwards with
 // their states and decays left in registers (4 states to a lane, so 128 of them), then back, so each
-// exponential is computed once.  The sums over n and over a warp's channels are butterflies that halve the
-// values as they go; a block's warps add their dB and dC in shared memory, and the blocks of a group's
-// channels leave partial rows that a second kernel adds in order.  Nothing is atomic.
+// exponential is computed once.  The working warps take the registers that the feeding warps give up.
+// dB and dC are sums over a warp's channels for each token and state: the lanes of neighbouring channels hold
+// their four states in different orders (xor by the channel's low bits), so that what a lane keeps of a sum
+// and what it hands over are always the same registers and a butterfly step is a shuffle and an addition.
+// The feeding warps add the block's warps in shared memory, and the blocks of a group's channels leave
+// partial rows that a second kernel adds in order.  Nothing is atomic.
 #include <algorithm>
+#include <type_traits>
 
 #include "ssm_common.cuh"
 
@@ -18,87 +22,338 @@ namespace {
 
 __device__ __forceinline__ int64_t tokens_of(const Seqs& s) { return s.cu ? s.T : s.T * s.n; }
 
-template <int NP>
+constexpr int kBwd = 4;  // states of a lane
+
+template <typename T, int NP, bool END>
 struct BwdShared {
-  float d[kWarps][Shape<NP>::CW][kRow];      // delta, then ddt
-  float x[kWarps][Shape<NP>::CW][kRow];      // x, then dx
-  float g[kWarps][Shape<NP>::CW][kRow];      // dy
-  float slope[kWarps][Shape<NP>::CW][kRow];  // softplus'
-  float b[kTile * NP], c[kTile * NP];
-  float red[kWarps][kTile][2 * NP];  // a warp's dB and dC of the tile
+  static constexpr int X = 512 / NP * kRow, S = NP * kRow;
+  float d[2][X], g[2][X], c[2][S];            // delta (then ddt), dy, C
+  float x[2][END ? 4 : X], b[2][END ? 4 : S]; // x (then dx), B
+  float slope[2][END ? 4 : X];                // softplus'
+  float red[2][END ? 1 : Shape<NP, kBwd>::WORK / 32][END ? 1 : kTile][END ? 4 : 2 * NP];  // a warp's dB and dC
+  // targets of 16-byte copies
+  alignas(16) RawRows<T, NP> rt;
+  alignas(16) RawRows<T, NP> rg;
+  alignas(16) typename std::conditional<END, float, RawRows<T, NP>>::type rx;
+  alignas(16) T rc[kRing<T, NP>][kTile * NP];
+  alignas(16) T rb[kRing<T, NP>][END ? 8 : kTile * NP];
 };
 
-// The gradient that leaves a segment at its front when none enters at its end, and the sum of its deltas.
-template <typename T, int NP>
-__global__ void __launch_bounds__(kWarps * 32) k_ssm_bwd_ends(Ssm s) {
-  using S = Shape<NP>;
-  constexpr int CW = S::CW;
-  __shared__ __align__(16) float sd[kWarps][CW][kRow], sg[kWarps][CW][kRow], sc[kTile * NP];
+// One segment, from its end.  END: only the gradient that leaves it at its front when none enters at its end,
+// and the sum of its deltas (the first pass over segments that have one before them).
+template <typename T, int NP, bool END>
+__global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
+  using S = Shape<NP, kBwd>;
+  constexpr int SPL = kBwd, NL = S::NL, CW = S::CW, FC = S::FC, WW = S::WORK / 32, PITCH = RawRows<T, NP>::PITCH, R = kRing<T, NP>;
+  extern __shared__ __align__(16) char raw[];
+  BwdShared<T, NP, END>& m = *reinterpret_cast<BwdShared<T, NP, END>*>(raw);
   if (bad_call(s.seqs)) return;
-  Place<NP> at;
-  if (!at.find(s, s.lg)) return;
+  Place<NP, SPL> at;
+  const bool unit = at.find(s, s.lg);
   const Piece& p = at.p;
-  if (p.idx == 0) return;
-  const int n0 = at.nl * 4;
-  float A2[4], ga[4] = {0.f, 0.f, 0.f, 0.f}, dsum[CW], bias[CW];
-  load_decay(s, at.ch, at.live, n0, A2);
-#pragma unroll
-  for (int i = 0; i < CW; ++i) {
-    dsum[i] = 0.f;
-    bias[i] = i < at.n && s.dt_bias ? s.dt_bias[at.c0 + i] : 0.f;
-  }
-  const T* dt = static_cast<const T*>(s.dt) + p.t0 * s.ld_dt + at.c0;
-  const T* dy = static_cast<const T*>(s.dy) + p.t0 * s.D + at.c0;
-  const T* Cm = static_cast<const T*>(s.Cm) + p.t0 * s.ld_c + (int64_t)at.g * s.N;
-  Cols<T, CW> gr, tr;
-  Mat<T, NP> cr;
-  auto fetch = [&](int t0) {
-    const int64_t t = t0 + at.lane;
-    const bool in = t < p.len;
-    tr.fetch(dt + t * s.ld_dt, in, s.vec, at.n);
-    gr.fetch(dy + t * s.D, in, s.vec, at.n);
-    cr.fetch(Cm + t0 * s.ld_c, s.ld_c, s.N, p.len - t0);
-  };
-  int t0 = (p.len - 1) / kTile * kTile;
-  fetch(t0);
-  for (; t0 >= 0; t0 -= kTile) {
-    const bool in = t0 + at.lane < p.len;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < CW; ++i) {
-      const float d = in && i < at.n ? softplus_acc(tr.get(i) + bias[i]) : 0.f;
-      sd[at.warp][i][at.lane] = d;
-      sg[at.warp][i][at.lane] = gr.get(i);
-      dsum[i] += d;
+  float* par = s.part_par + ((int64_t)blockIdx.x * s.D + at.ch) * (s.N + 2);
+  if (!unit) {  // no such segment: its sums are empty
+    if (!END && at.live) {
+      for (int j = at.n0; j < at.n0 + SPL; ++j)
+        if (j < s.N) par[j] = 0.f;
+      if (at.nl == 0) par[s.N] = par[s.N + 1] = 0.f;
     }
-    cr.stage(sc);
+    return;
+  }
+  if (END && p.idx == 0) return;  // nothing precedes
+  const int tiles = (p.len + kTile - 1) / kTile;
+
+  if (at.feeds) {
+    if (!END) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    const Inputs<T, NP, SPL> in(s, at);
+    float bias[FC];
+#pragma unroll
+    for (int i = 0; i < FC; ++i) bias[i] = at.sc + i < at.width && s.dt_bias ? s.dt_bias[at.c0 + at.sc + i] : 0.f;
+    const int64_t row = (p.t0 + at.tok) * s.D + at.c0 + at.sc;
+    T *dx = static_cast<T*>(s.dx) + row, *ddt = static_cast<T*>(s.ddt) + row;
+    float* pbc = s.part_bc + ((at.tile * tokens_of(s.seqs) + p.t0) * s.G + at.g) * 2 * NP;
+    auto fetch = [&](int i, int r) {
+      if (i < tiles) {
+        const int t0 = (tiles - 1 - i) * kTile, n = p.len - t0;
+        in.dt.fetch(m.rt.v[r], at.f, t0, n);
+        in.dy.fetch(m.rg.v[r], at.f, t0, n);
+        in.C.fetch(m.rc[r], at.f, t0, n);
+        if constexpr (!END) {
+          in.x.fetch(m.rx.v[r], at.f, t0, n);
+          in.B.fetch(m.rb[r], at.f, t0, n);
+        }
+      }
+      copy_commit();
+    };
+    auto widen = [&](int i, int r, int buf) {
+      const bool here = (tiles - 1 - i) * kTile + at.tok < p.len;
+      Cols<T, FC> xr, tr, gr;
+      tr.load(m.rt.v[r] + at.tok * PITCH + at.sc);
+      gr.load(m.rg.v[r] + at.tok * PITCH + at.sc);
+      if constexpr (!END) xr.load(m.rx.v[r] + at.tok * PITCH + at.sc);
+      const int to = at.sc * kRow + at.tok;
+#pragma unroll
+      for (int k = 0; k < FC; k += 2) {
+        float2 e;
+        const float2 v = {tr.get(k) + bias[k], tr.get(k + 1) + bias[k + 1]}, d = softplus2(v, e);
+        m.d[buf][to + k * kRow] = here ? d.x : 0.f;
+        m.d[buf][to + (k + 1) * kRow] = here ? d.y : 0.f;
+        m.g[buf][to + k * kRow] = gr.get(k);
+        m.g[buf][to + (k + 1) * kRow] = gr.get(k + 1);
+        if constexpr (!END) {
+          m.x[buf][to + k * kRow] = xr.get(k);
+          m.x[buf][to + (k + 1) * kRow] = xr.get(k + 1);
+          m.slope[buf][to + k * kRow] = here ? softplus_slope(v.x, e.x) : 0.f;
+          m.slope[buf][to + (k + 1) * kRow] = here ? softplus_slope(v.y, e.y) : 0.f;
+        }
+      }
+      widen_states<T, NP, SPL>(m.c[buf], m.rc[r], at.f);
+      if constexpr (!END) widen_states<T, NP, SPL>(m.b[buf], m.rb[r], at.f);
+    };
+    // the gradients out of their inputs' places, and the sums over the block's channels
+    auto put = [&](int i, int buf) {
+      if constexpr (!END) {
+        const int t0 = (tiles - 1 - i) * kTile, from = at.sc * kRow + at.tok;
+        Cols<T, FC> ox, od;
+        const bool here = t0 + at.tok < p.len;
+#pragma unroll
+        for (int k = 0; k < FC; ++k) {
+          ox.put(k, m.x[buf][from + k * kRow]);
+          od.put(k, m.d[buf][from + k * kRow]);
+        }
+        if (here) {
+          ox.store(dx + (int64_t)t0 * s.D, s.vec, at.width - at.sc);
+          od.store(ddt + (int64_t)t0 * s.D, s.vec, at.width - at.sc);
+        }
+        const int n = min(kTile, p.len - t0) * (NP / 2);
+        for (int e = at.f; e < n; e += kFeed) {
+          const int t = e / (NP / 2), v = e % (NP / 2) * 4;
+          float4 a = ld4(&m.red[buf][0][t][v]);
+#pragma unroll
+          for (int w = 1; w < WW; ++w) {
+            const float4 o = ld4(&m.red[buf][w][t][v]);
+            a.x += o.x, a.y += o.y, a.z += o.z, a.w += o.w;
+          }
+          *reinterpret_cast<float4*>(pbc + (int64_t)(t0 + t) * s.G * 2 * NP + v) = a;
+        }
+      }
+    };
+    // The feeding warps meet on a barrier of their own before they widen what all of them fetched.
+    auto meet = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    for (int k = 0; k < R; ++k) fetch(k, k);
+    int r = 0;
+    for (int i = 0; i < tiles; ++i) {  // tile i (from the end) is widened while the one before it is worked on
+      copy_wait<R - 1>();
+      meet();
+      if (i > 1) put(i - 2, i & 1);
+      widen(i, r, i & 1);
+      meet();
+      fetch(i + R, r);
+      r = r == R - 1 ? 0 : r + 1;
+      __syncthreads();
+    }
+    copy_wait<0>();
     __syncthreads();
-    if (t0 > 0) fetch(t0 - kTile);
-#pragma unroll 2
-    for (int q = kTile / 4 - 1; q >= 0; --q) {
-      const float4 dv = *reinterpret_cast<const float4*>(&sd[at.warp][at.cl][4 * q]);
-      const float4 gv = *reinterpret_cast<const float4*>(&sg[at.warp][at.cl][4 * q]);
-      const float d4[4] = {dv.x, dv.y, dv.z, dv.w}, g4[4] = {gv.x, gv.y, gv.z, gv.w};
+    if (tiles > 1) put(tiles - 2, tiles & 1);
+    if (tiles > 0) put(tiles - 1, (tiles - 1) & 1);
+    return;
+  }
+
+  if (!END) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+  // register j of a lane belongs to state n0 + (j ^ pm)
+  const int pm = CW >= 4 ? at.cl & 3 : at.cl & 1;
+  float A2[SPL], ga[SPL];
+  float2 dA[SPL];
+  int row[SPL];
 #pragma unroll
-      for (int k = 3; k >= 0; --k) {
-        const float4 cv = *reinterpret_cast<const float4*>(&sc[(4 * q + k) * NP + n0]);
-        const float c4[4] = {cv.x, cv.y, cv.z, cv.w};
+  for (int j = 0; j < SPL; ++j) {
+    const int n = at.n0 + (j ^ pm);
+    A2[j] = at.live && n < s.N ? decay_rate(s.A_log[at.ch * s.N + n]) : 0.f;
+    ga[j] = 0.f;
+    dA[j] = {0.f, 0.f};
+    row[j] = state_row<NP, SPL>(n);
+    if (!END && at.live) {
+      if (s.cut && p.pos + p.len < p.slen)
+        ga[j] = s.starts[state_at<NP>(s, blockIdx.x, at.ch, n)];
+      else if (s.dfinal && n < s.N)
+        ga[j] = s.dfinal[((int64_t)p.seq * s.D + at.ch) * s.N + n];
+    }
+  }
+  const float skip = at.live && s.skip ? s.skip[at.ch] : 0.f;
+  const float* ck = END ? nullptr : s.ckpt + state_at<NP>(s, first_unit(s.seqs, p.seq, kCkptLog) + p.pos / kCkpt, at.ch, at.n0);
+  const int slot = lane_slot<4, NL>(at.nl);
+  float total = 0.f, dskip = 0.f, dbias = 0.f;
+  // the state that enters the 16 tokens to come, asked for 16 tokens early
+  int chunk = (p.len - 1) / kCkpt;
+  float ahead[SPL];
+  auto enter = [&](int k) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ga[j] = ex2(d4[k] * A2[j]) * fmaf(c4[j], g4[k], ga[j]);
+    for (int j = 0; j < SPL; ++j) ahead[j] = at.live ? ck[(int64_t)max(k, 0) * s.D * NP + (j ^ pm)] : 0.f;
+  };
+  if constexpr (!END) enter(chunk);
+  for (int i = 0; i < tiles; ++i) {
+    const int buf = i & 1, t0 = (tiles - 1 - i) * kTile;
+    __syncthreads();  // the tile is there
+    float tsum = 0.f;
+#pragma unroll 1
+    for (int sub = p.len - t0 > kCkpt ? 1 : 0; sub >= 0; --sub) {
+      float* d = m.d[buf] + at.c * kRow + sub * kCkpt;
+      const float* g = m.g[buf] + at.c * kRow + sub * kCkpt;
+      const float* c = m.c[buf] + sub * kCkpt;
+      if constexpr (END) {
+        float dq[kCkpt / 4];
+#pragma unroll
+        for (int q = kCkpt / 4 - 1; q >= 0; --q) {
+          const float4 dv = ld4(d + 4 * q), gv = ld4(g + 4 * q);
+          dq[q] = (dv.x + dv.y) + (dv.z + dv.w);
+          const float2 d2[2] = {{dv.x, dv.y}, {dv.z, dv.w}}, g2[2] = {{gv.x, gv.y}, {gv.z, gv.w}};
+#pragma unroll
+          for (int j = 0; j < SPL; ++j) {
+            const float4 cv = ld4(c + row[j] + 4 * q);
+            const float2 c2[2] = {{cv.x, cv.y}, {cv.z, cv.w}};
+#pragma unroll
+            for (int k = 1; k >= 0; --k) {
+              const float2 e = __fmul2_rn(d2[k], {A2[j], A2[j]});
+              ga[j] = ex2(e.y) * fmaf(c2[k].y, g2[k].y, ga[j]);
+              ga[j] = ex2(e.x) * fmaf(c2[k].x, g2[k].x, ga[j]);
+            }
+          }
+        }
+        tsum += (dq[0] + dq[1]) + (dq[2] + dq[3]);
+      } else {
+        float* x = m.x[buf] + at.c * kRow + sub * kCkpt;
+        const float* b = m.b[buf] + sub * kCkpt;
+        const float* slope = m.slope[buf] + at.c * kRow + sub * kCkpt;
+        float h0[SPL], h[kCkpt][SPL], a[kCkpt][SPL];
+#pragma unroll
+        for (int j = 0; j < SPL; ++j) h0[j] = ahead[j];
+        enter(--chunk);
+#pragma unroll
+        for (int q = 0; q < kCkpt / 4; ++q) {
+          const float4 dv = ld4(d + 4 * q), xv = ld4(x + 4 * q);
+          const float2 d2[2] = {{dv.x, dv.y}, {dv.z, dv.w}}, x2[2] = {{xv.x, xv.y}, {xv.z, xv.w}};
+#pragma unroll
+          for (int j = 0; j < SPL; ++j) {
+            const float4 bv = ld4(b + row[j] + 4 * q);
+            const float2 b2[2] = {{bv.x, bv.y}, {bv.z, bv.w}};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int t = 4 * q + 2 * k;
+              const float2 e = __fmul2_rn(d2[k], {A2[j], A2[j]}), u = __fmul2_rn(__fmul2_rn(d2[k], x2[k]), b2[k]);
+              a[t][j] = ex2(e.x);
+              a[t + 1][j] = ex2(e.y);
+              h[t][j] = fmaf(a[t][j], t > 0 ? h[t > 0 ? t - 1 : 0][j] : h0[j], u.x);
+              h[t + 1][j] = fmaf(a[t + 1][j], h[t][j], u.y);
+            }
+          }
+        }
+#pragma unroll
+        for (int q = kCkpt / 4 - 1; q >= 0; --q) {
+          const float4 dv = ld4(d + 4 * q), xv = ld4(x + 4 * q), gv = ld4(g + 4 * q);
+          const float2 d2[2] = {{dv.x, dv.y}, {dv.z, dv.w}}, x2[2] = {{xv.x, xv.y}, {xv.z, xv.w}}, g2[2] = {{gv.x, gv.y}, {gv.z, gv.w}};
+          float4 bv[SPL], cv[SPL];
+#pragma unroll
+          for (int j = 0; j < SPL; ++j) bv[j] = ld4(b + row[j] + 4 * q), cv[j] = ld4(c + row[j] + 4 * q);
+          float du[4], sq[4];
+#pragma unroll
+          for (int k = 1; k >= 0; --k) {
+            const int t = 4 * q + 2 * k;
+            const float2 u = __fmul2_rn(d2[k], x2[k]);
+            float2 du2 = {0.f, 0.f}, sq2 = {0.f, 0.f}, vb[SPL], vc[SPL];
+#pragma unroll
+            for (int j = 0; j < SPL; ++j) {
+              const float2 b2 = k ? float2{bv[j].z, bv[j].w} : float2{bv[j].x, bv[j].y};
+              const float2 c2 = k ? float2{cv[j].z, cv[j].w} : float2{cv[j].x, cv[j].y};
+              float2 gg, q2;
+              gg.y = fmaf(c2.y, g2[k].y, ga[j]);
+              const float g1 = a[t + 1][j] * gg.y;
+              gg.x = fmaf(c2.x, g2[k].x, g1);
+              ga[j] = a[t][j] * gg.x;
+              q2.y = g1 * h[t][j];
+              q2.x = ga[j] * (t > 0 ? h[t > 0 ? t - 1 : 0][j] : h0[j]);
+              vb[j] = __fmul2_rn(gg, u);
+              vc[j] = __fmul2_rn(g2[k], {h[t][j], h[t + 1][j]});
+              du2 = __ffma2_rn(gg, b2, du2);
+              sq2 = __ffma2_rn({A2[j], A2[j]}, q2, sq2);
+              dA[j] = __ffma2_rn(d2[k], q2, dA[j]);
+            }
+            du[2 * k] = du2.x, du[2 * k + 1] = du2.y;
+            sq[2 * k] = sq2.x, sq[2 * k + 1] = sq2.y;
+            auto step = [&](float2& keep, const float2& give, int lanes) {
+              keep = __fadd2_rn(keep, {__shfl_xor_sync(0xffffffffu, give.x, lanes), __shfl_xor_sync(0xffffffffu, give.y, lanes)});
+            };
+            float* red = &m.red[buf][at.warp][sub * kCkpt + t][at.n0];
+            if constexpr (CW >= 4) {
+              step(vb[0], vb[2], 2 * NL), step(vb[1], vb[3], 2 * NL);
+              step(vc[0], vc[2], 2 * NL), step(vc[1], vc[3], 2 * NL);
+              step(vb[0], vb[1], NL), step(vc[0], vc[1], NL);
+              if constexpr (CW >= 8) step(vb[0], vb[0], 4 * NL), step(vc[0], vc[0], 4 * NL);
+              if constexpr (CW >= 16) step(vb[0], vb[0], 8 * NL), step(vc[0], vc[0], 8 * NL);
+              if constexpr (CW >= 8) {  // lanes with the same sums: one writes dB, one dC
+                const bool second = at.cl & 4;
+                if (CW < 16 || at.cl < 8) {
+                  red[(second ? NP : 0) + pm] = second ? vc[0].x : vb[0].x;
+                  red[2 * NP + (second ? NP : 0) + pm] = second ? vc[0].y : vb[0].y;
+                }
+              } else {
+                red[pm] = vb[0].x, red[NP + pm] = vc[0].x;
+                red[2 * NP + pm] = vb[0].y, red[3 * NP + pm] = vc[0].y;
+              }
+            } else {
+              step(vb[0], vb[1], NL), step(vb[2], vb[3], NL), step(vc[0], vc[1], NL), step(vc[2], vc[3], NL);
+#pragma unroll
+              for (int j = 0; j < 4; j += 2) {
+                red[j ^ pm] = vb[j].x, red[NP + (j ^ pm)] = vc[j].x;
+                red[2 * NP + (j ^ pm)] = vb[j].y, red[3 * NP + (j ^ pm)] = vc[j].y;
+              }
+            }
+          }
+          lane_sums<4, NL, 1>(du, at.lane);
+          lane_sums<4, NL, 1>(sq, at.lane);
+          __syncwarp();
+          if (at.nl < 4) {  // the gradients take their inputs' places
+            constexpr int M = NL < 4 ? 4 / NL : 1;
+#pragma unroll
+            for (int k = 0; k < M; ++k) {
+              const int t = 4 * q + slot + k;
+              const float dd = d[t], xx = x[t], gy = g[t];
+              const float o = fmaf(xx, du[k], kLn2 * sq[k]) * slope[t];
+              x[t] = fmaf(dd, du[k], skip * gy);
+              d[t] = o;
+              dskip = fmaf(gy, xx, dskip);
+              dbias += o;
+            }
+          }
+        }
       }
     }
+    total += tsum;
   }
-  float total = 0.f;
+  __syncthreads();
+  if constexpr (!END) {
 #pragma unroll
-  for (int i = 0; i < CW; ++i) {
-    float v = dsum[i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (i == at.cl) total = v;
+    for (int o = 1; o < NL; o <<= 1) {
+      dskip += __shfl_xor_sync(0xffffffffu, dskip, o);
+      dbias += __shfl_xor_sync(0xffffffffu, dbias, o);
+    }
   }
-  if (at.live) {
-    *reinterpret_cast<float4*>(s.starts + state_at<NP>(s, blockIdx.x, at.ch, n0)) = make_float4(ga[0], ga[1], ga[2], ga[3]);
+  if (!at.live) return;
+  if constexpr (END) {
+#pragma unroll
+    for (int j = 0; j < SPL; ++j) s.starts[state_at<NP>(s, blockIdx.x, at.ch, at.n0 + (j ^ pm))] = ga[j];
     if (at.nl == 0) s.sums[(int64_t)blockIdx.x * s.D + at.ch] = total;
+  } else {
+#pragma unroll
+    for (int j = 0; j < SPL; ++j) {
+      const int n = at.n0 + (j ^ pm);
+      if (n >= s.N) continue;
+      par[n] = dA[j].x + dA[j].y;
+      if (s.dinit && p.idx == 0) s.dinit[((int64_t)p.seq * s.D + at.ch) * s.N + n] = ga[j];
+    }
+    if (at.nl == 0) {
+      par[s.N] = dskip;
+      par[s.N + 1] = dbias;
+    }
   }
 }
 
@@ -123,203 +378,6 @@ __global__ void __launch_bounds__(256) k_ssm_bwd_join(Ssm s) {
   }
 }
 
-template <typename T, int NP>
-__global__ void __launch_bounds__(kWarps * 32) k_ssm_bwd(Ssm s) {
-  using S = Shape<NP>;
-  constexpr int NL = S::NL, CW = S::CW;
-  extern __shared__ __align__(16) char raw[];
-  BwdShared<NP>& m = *reinterpret_cast<BwdShared<NP>*>(raw);
-  if (bad_call(s.seqs)) return;
-  Place<NP> at;
-  const bool unit = at.find(s, s.lg);
-  const Piece& p = at.p;
-  const int n0 = at.nl * 4;
-  float* par = s.part_par + ((int64_t)blockIdx.x * s.D + at.ch) * (s.N + 2);
-  if (!unit) {  // no such segment: its sums are empty
-    if (at.live) {
-      for (int j = n0; j < n0 + 4; ++j)
-        if (j < s.N) par[j] = 0.f;
-      if (at.nl == 0) par[s.N] = par[s.N + 1] = 0.f;
-    }
-    return;
-  }
-  float A2[4], ga[4] = {0.f, 0.f, 0.f, 0.f}, dA[4] = {0.f, 0.f, 0.f, 0.f};
-  load_decay(s, at.ch, at.live, n0, A2);
-  if (at.live) {
-    if (s.cut && p.pos + p.len < p.slen) {
-      const float4 v = *reinterpret_cast<const float4*>(s.starts + state_at<NP>(s, blockIdx.x, at.ch, n0));
-      ga[0] = v.x, ga[1] = v.y, ga[2] = v.z, ga[3] = v.w;
-    } else if (s.dfinal) {
-      load_states(s.dfinal + ((int64_t)p.seq * s.D + at.ch) * s.N, s.N, n0, ga);
-    }
-  }
-  const float skip = at.live && s.skip ? s.skip[at.ch] : 0.f;
-  float dskip = 0.f, dbias = 0.f;
-  float bias[CW];
-#pragma unroll
-  for (int i = 0; i < CW; ++i) bias[i] = i < at.n && s.dt_bias ? s.dt_bias[at.c0 + i] : 0.f;
-  const T* x = static_cast<const T*>(s.x) + p.t0 * s.ld_x + at.c0;
-  const T* dt = static_cast<const T*>(s.dt) + p.t0 * s.ld_dt + at.c0;
-  const T* dy = static_cast<const T*>(s.dy) + p.t0 * s.D + at.c0;
-  const T* Bm = static_cast<const T*>(s.Bm) + p.t0 * s.ld_b + (int64_t)at.g * s.N;
-  const T* Cm = static_cast<const T*>(s.Cm) + p.t0 * s.ld_c + (int64_t)at.g * s.N;
-  T* dx = static_cast<T*>(s.dx) + p.t0 * s.D + at.c0;
-  T* ddt = static_cast<T*>(s.ddt) + p.t0 * s.D + at.c0;
-  const float* ck = s.ckpt + state_at<NP>(s, first_unit(s.seqs, p.seq, kCkptLog) + p.pos / kCkpt, at.ch, n0);
-  const int64_t tiles = (s.D / s.G + S::CC - 1) / S::CC;
-  float* pbc = s.part_bc + (((blockIdx.y - at.g * tiles) * tokens_of(s.seqs) + p.t0) * s.G + at.g) * 2 * NP;
-  const int slot = lane_slot<4, NL>(at.nl);
-  constexpr int BC = CW >= 8 ? 1 : 8 / CW;  // values of dB and dC that a lane is left with
-  const int bcs = lane_slot<8, CW>(at.cl), bcat = bcs / 4 * NP + n0 + bcs % 4;
-  const bool bcw = at.cl < 8;
-
-  Cols<T, CW> xr, tr, gr;
-  Mat<T, NP> br, cr;
-  auto fetch = [&](int t0) {
-    const int64_t t = t0 + at.lane;
-    const bool in = t < p.len;
-    xr.fetch(x + t * s.ld_x, in, s.vec, at.n);
-    tr.fetch(dt + t * s.ld_dt, in, s.vec, at.n);
-    gr.fetch(dy + t * s.D, in, s.vec, at.n);
-    br.fetch(Bm + t0 * s.ld_b, s.ld_b, s.N, p.len - t0);
-    cr.fetch(Cm + t0 * s.ld_c, s.ld_c, s.N, p.len - t0);
-  };
-  int t0 = p.len > 0 ? (p.len - 1) / kTile * kTile : -1;
-  if (t0 >= 0) fetch(t0);
-  for (; t0 >= 0; t0 -= kTile) {
-    const bool in = t0 + at.lane < p.len;
-#pragma unroll
-    for (int i = 0; i < CW; ++i) {
-      float d = 0.f, sl = 0.f;
-      if (in && i < at.n) {
-        const float v = tr.get(i) + bias[i];
-        d = softplus_acc(v);
-        sl = v > 20.f ? 1.f : rcp(1.f + exp_acc(-v));
-      }
-      m.d[at.warp][i][at.lane] = d;
-      m.slope[at.warp][i][at.lane] = sl;
-      m.x[at.warp][i][at.lane] = xr.get(i);
-      m.g[at.warp][i][at.lane] = gr.get(i);
-    }
-    br.stage(m.b);
-    cr.stage(m.c);
-    __syncthreads();
-    if (t0 > 0) fetch(t0 - kTile);
-    const int subs = p.len - t0 > kCkpt ? 2 : 1;
-    for (int sub = subs - 1; sub >= 0; --sub) {
-      float h0[4] = {0.f, 0.f, 0.f, 0.f}, h[kCkpt][4], a[kCkpt][4];
-      if (at.live) {
-        const float4 v = *reinterpret_cast<const float4*>(ck + (int64_t)(t0 / kCkpt + sub) * s.D * NP);
-        h0[0] = v.x, h0[1] = v.y, h0[2] = v.z, h0[3] = v.w;
-      }
-      const int ts = sub * kCkpt;
-#pragma unroll
-      for (int q = 0; q < kCkpt / 4; ++q) {
-        const float4 dv = *reinterpret_cast<const float4*>(&m.d[at.warp][at.cl][ts + 4 * q]);
-        const float4 xv = *reinterpret_cast<const float4*>(&m.x[at.warp][at.cl][ts + 4 * q]);
-        const float d4[4] = {dv.x, dv.y, dv.z, dv.w}, x4[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int t = 4 * q + k;
-          const float4 bv = *reinterpret_cast<const float4*>(&m.b[(ts + t) * NP + n0]);
-          const float b4[4] = {bv.x, bv.y, bv.z, bv.w};
-          const float u = d4[k] * x4[k];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            a[t][j] = ex2(d4[k] * A2[j]);
-            h[t][j] = fmaf(a[t][j], t > 0 ? h[t > 0 ? t - 1 : 0][j] : h0[j], u * b4[j]);
-          }
-        }
-      }
-#pragma unroll
-      for (int q = kCkpt / 4 - 1; q >= 0; --q) {
-        const float4 dv = *reinterpret_cast<const float4*>(&m.d[at.warp][at.cl][ts + 4 * q]);
-        const float4 xv = *reinterpret_cast<const float4*>(&m.x[at.warp][at.cl][ts + 4 * q]);
-        const float4 gv = *reinterpret_cast<const float4*>(&m.g[at.warp][at.cl][ts + 4 * q]);
-        const float d4[4] = {dv.x, dv.y, dv.z, dv.w}, x4[4] = {xv.x, xv.y, xv.z, xv.w}, g4[4] = {gv.x, gv.y, gv.z, gv.w};
-        float du[4], sq[4];
-#pragma unroll
-        for (int k = 3; k >= 0; --k) {
-          const int t = 4 * q + k;
-          const float4 bv = *reinterpret_cast<const float4*>(&m.b[(ts + t) * NP + n0]);
-          const float4 cv = *reinterpret_cast<const float4*>(&m.c[(ts + t) * NP + n0]);
-          const float b4[4] = {bv.x, bv.y, bv.z, bv.w}, c4[4] = {cv.x, cv.y, cv.z, cv.w};
-          const float u = d4[k] * x4[k];
-          float bc[8];
-          du[k] = sq[k] = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float g = fmaf(c4[j], g4[k], ga[j]);
-            bc[j] = g * u;
-            bc[4 + j] = g4[k] * h[t][j];
-            du[k] = fmaf(g, b4[j], du[k]);
-            ga[j] = a[t][j] * g;
-            const float qv = ga[j] * (t > 0 ? h[t > 0 ? t - 1 : 0][j] : h0[j]);
-            sq[k] = fmaf(A2[j], qv, sq[k]);
-            dA[j] = fmaf(d4[k], qv, dA[j]);
-          }
-          lane_sums<8, CW, NL>(bc, at.lane);
-          if (bcw) {
-#pragma unroll
-            for (int i = 0; i < BC; ++i) m.red[at.warp][ts + t][bcat + i] = bc[i];
-          }
-        }
-        lane_sums<4, NL, 1>(du, at.lane);
-        lane_sums<4, NL, 1>(sq, at.lane);
-        __syncwarp();
-        if (at.nl < 4) {  // the gradients take their inputs' places
-          constexpr int M = NL < 4 ? 4 / NL : 1;
-#pragma unroll
-          for (int k = 0; k < M; ++k) {
-            const int t = ts + 4 * q + slot + k;
-            float &d = m.d[at.warp][at.cl][t], &xx = m.x[at.warp][at.cl][t];
-            const float dyv = m.g[at.warp][at.cl][t];
-            const float dd = fmaf(xx, du[k], kLn2 * sq[k]) * m.slope[at.warp][at.cl][t];
-            const float dxv = fmaf(d, du[k], skip * dyv);
-            dskip = fmaf(dyv, xx, dskip);
-            dbias += dd;
-            d = dd;
-            xx = dxv;
-          }
-        }
-      }
-    }
-    __syncthreads();
-    {
-      Cols<T, CW> ox, od;
-#pragma unroll
-      for (int i = 0; i < CW; ++i) {
-        ox.put(i, m.x[at.warp][i][at.lane]);
-        od.put(i, m.d[at.warp][i][at.lane]);
-      }
-      ox.store(dx + (int64_t)(t0 + at.lane) * s.D, in, s.vec, at.n);
-      od.store(ddt + (int64_t)(t0 + at.lane) * s.D, in, s.vec, at.n);
-    }
-    const int n = min(kTile, p.len - t0) * 2 * NP;
-    for (int e = threadIdx.x; e < n; e += kWarps * 32) {
-      const int t = e / (2 * NP), v = e % (2 * NP);
-      float r = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) r += m.red[w][t][v];
-      pbc[(int64_t)(t0 + t) * s.G * 2 * NP + v] = r;
-    }
-    __syncwarp();
-  }
-#pragma unroll
-  for (int o = 1; o < NL; o <<= 1) {
-    dskip += __shfl_xor_sync(0xffffffffu, dskip, o);
-    dbias += __shfl_xor_sync(0xffffffffu, dbias, o);
-  }
-  if (!at.live) return;
-  for (int j = 0; j < 4; ++j)
-    if (n0 + j < s.N) par[n0 + j] = dA[j];
-  if (at.nl == 0) {
-    par[s.N] = dskip;
-    par[s.N + 1] = dbias;
-  }
-  if (s.dinit && p.idx == 0) store_states(s.dinit + ((int64_t)p.seq * s.D + at.ch) * s.N, s.N, n0, ga);
-}
-
 // dB and dC of a token and group: the channel tiles in order.
 template <typename T>
 __global__ void __launch_bounds__(256) k_ssm_bc_sums(Ssm s, int NP, int64_t tiles) {
@@ -334,24 +392,16 @@ __global__ void __launch_bounds__(256) k_ssm_bc_sums(Ssm s, int NP, int64_t tile
   }
 }
 
-// The parameters' gradients: 32 columns of [D][N + 2] by 32 strands of units, the strands in a fixed tree.
-__global__ void __launch_bounds__(1024) k_ssm_par_sums(Ssm s, int64_t units) {
-  __shared__ float red[32][33];
+// The parameters' gradients: columns of [D][N + 2], summed over the units.
+template <int STR>
+__global__ void __launch_bounds__(STR == 1 ? 256 : 32 * STR) k_ssm_par_sums(Ssm s, int64_t units) {
   if (bad_call(s.seqs)) return;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t width = s.D * (s.N + 2), c = (int64_t)blockIdx.x * 32 + tx;
-  float a = 0.f;
-  if (c < width)
-    for (int64_t u = ty; u < units; u += 32) a += s.part_par[u * width + c];
-  red[ty][tx] = a;
-  __syncthreads();
-  float v = red[tx][ty];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int64_t cc = (int64_t)blockIdx.x * 32 + ty;
-  if (tx != 0 || cc >= width) return;
-  const int64_t ch = cc / (s.N + 2);
-  const int n = (int)(cc - ch * (s.N + 2));
+  const int64_t width = s.D * (s.N + 2);
+  int64_t c;
+  const float v = strand_sums<STR>(s.part_par, units, width, width, c);
+  if (c < 0) return;
+  const int64_t ch = c / (s.N + 2);
+  const int n = (int)(c - ch * (s.N + 2));
   if (n < s.N) {
     if (s.dA_log) s.dA_log[ch * s.N + n] = -expf(s.A_log[ch * s.N + n]) * v;
   } else if (n == s.N) {
@@ -363,22 +413,28 @@ __global__ void __launch_bounds__(1024) k_ssm_par_sums(Ssm s, int64_t units) {
 
 template <typename T, int NP>
 cudaError_t backward(const Ssm& c, cudaStream_t s) {
-  using S = Shape<NP>;
+  using S = Shape<NP, kBwd>;
   const int64_t Dg = c.D / c.G, tiles = (Dg + S::CC - 1) / S::CC, units = max_units(c.seqs, c.lg);
   const dim3 grid((unsigned)units, (unsigned)(c.G * tiles));
   if (c.cut) {
     {
       ProfScope ps("ssm_bwd_ends", s);
-      k_ssm_bwd_ends<T, NP><<<grid, kWarps * 32, 0, s>>>(c);
+      constexpr size_t bytes = sizeof(BwdShared<T, NP, true>);
+      if (cudaError_t e = allow_shared(k_ssm_bwd<T, NP, true>, bytes)) return e;
+      k_ssm_bwd<T, NP, true><<<grid, S::NT, bytes, s>>>(c);
     }
     ProfScope ps("ssm_bwd_join", s);
     k_ssm_bwd_join<NP><<<(unsigned)((c.D * NP + 255) / 256 * c.seqs.n), 256, 0, s>>>(c);
   }
-  cudaError_t e = cudaFuncSetAttribute(k_ssm_bwd<T, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(BwdShared<NP>));
-  if (e != cudaSuccess) return e;
   {
     ProfScope ps("ssm_bwd", s);
-    k_ssm_bwd<T, NP><<<grid, kWarps * 32, sizeof(BwdShared<NP>), s>>>(c);
+    constexpr size_t bytes = sizeof(BwdShared<T, NP, false>);
+    if (cudaError_t e = allow_shared(k_ssm_bwd<T, NP, false>, bytes)) return e;
+    // the working warps' 192 registers and the feeding warps' 64 are the launch's 128 a thread, no more
+    cudaFuncAttributes f;
+    if (cudaError_t e = cudaFuncGetAttributes(&f, k_ssm_bwd<T, NP, false>)) return e;
+    if (f.numRegs != 128) return cudaErrorInvalidConfiguration;
+    k_ssm_bwd<T, NP, false><<<grid, S::NT, bytes, s>>>(c);
   }
   const int64_t all = (c.seqs.cu ? c.seqs.T : c.seqs.T * c.seqs.n) * c.G * 2 * NP;
   if (all > 0) {
@@ -386,7 +442,12 @@ cudaError_t backward(const Ssm& c, cudaStream_t s) {
     k_ssm_bc_sums<T><<<(unsigned)std::min<int64_t>((all + 255) / 256, 148 * 32), 256, 0, s>>>(c, NP, tiles);
   }
   ProfScope ps("ssm_bwd_par", s);
-  k_ssm_par_sums<<<(unsigned)((c.D * (c.N + 2) + 31) / 32), 1024, 0, s>>>(c, units);
+  const int64_t width = c.D * (c.N + 2);
+  switch (sum_strands(units)) {
+    case 1: k_ssm_par_sums<1><<<(unsigned)((width + 255) / 256), 256, 0, s>>>(c, units); break;
+    case 8: k_ssm_par_sums<8><<<(unsigned)((width + 31) / 32), 256, 0, s>>>(c, units); break;
+    default: k_ssm_par_sums<32><<<(unsigned)((width + 31) / 32), 1024, 0, s>>>(c, units);
+  }
   return cudaGetLastError();
 }
 

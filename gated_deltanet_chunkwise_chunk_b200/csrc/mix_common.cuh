@@ -160,5 +160,40 @@ __device__ __forceinline__ bool bad_call(const Seqs& s) {
   return false;
 }
 
+// The sum over rows r < n of part[r * ld + c]: STR strands of rows for each column, each in row order, the strands
+// in a fixed tree.  Returns it with its column c to one thread a column, c = -1 to the others.
+template <int STR>
+__device__ __forceinline__ float strand_sums(const float* __restrict__ part, int64_t n, int64_t ld, int64_t width, int64_t& c) {
+  if constexpr (STR == 1) {
+    c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    float a = 0.f;
+    if (c < width) {
+#pragma unroll 4
+      for (int64_t r = 0; r < n; ++r) a += part[r * ld + c];
+    } else {
+      c = -1;
+    }
+    return a;
+  } else {
+    __shared__ float red[32][STR + 1];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int64_t from = (int64_t)blockIdx.x * 32 + tx;
+    float a = 0.f;
+    if (from < width) {
+#pragma unroll 4
+      for (int64_t r = ty; r < n; r += STR) a += part[r * ld + from];
+    }
+    red[tx][ty] = a;
+    __syncthreads();
+    const int col = threadIdx.x / STR, strand = threadIdx.x % STR;
+    float v = red[col][strand];
+#pragma unroll
+    for (int o = STR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    c = (int64_t)blockIdx.x * 32 + col;
+    if (strand != 0 || c >= width) c = -1;
+    return v;
+  }
+}
+
 }  // namespace mix
 }  // namespace gdn

@@ -5,39 +5,49 @@
 //
 // The states of a channel never mix with another channel's, so the work of a token is D x N independent
 // recurrences, each an exponential and about four multiply-adds: no matrix product has these entries (the
-// decay differs in t, d and n), and the exponentials bound it: 16 per clock and multiprocessor.
+// decay differs in t, d and n).  Exponentials (16 per clock and multiprocessor) and instruction issue bound it.
 //
-// A warp walks over the tokens of a piece of a sequence with one channel and four states to a lane: lane
-// (cl, nl) holds states 4 nl .. 4 nl + 3 of channel cl, NL = NP / 4 lanes to a channel (NP: N rounded up to a
-// power of two) and CW = 32 / NL channels to a warp.  So few states to a lane (instead of, say, four channels
-// by four states) make as many warps as there are, and one sequence of a wide layer then fills the card
-// without being cut along time, which would cost a second pass of exponentials.
-// Tiles of 32 tokens are staged in shared memory: a lane fetches one token's CW channels of x and dt, applies
-// the softplus once and leaves them token-contiguous, so that a state lane reads four tokens with one load;
-// B and C are shared by the block's warps.  Tokens past the piece's end are staged as delta = x = 0, which
-// leaves every state as it is.
+// A warp walks over the tokens of a segment with one channel and SPL states to a lane: lane (cl, nl) holds
+// states SPL nl .. of channel cl, NL = NP / SPL lanes to a channel (NP: N rounded up to a power of two) and
+// CW = 32 / NL channels to a warp; a block has CC = 512 / NP channels in 16 / SPL such warps, and four more
+// warps that feed them.  Tiles of 32 tokens arrive in shared memory three deep by asynchronous copies; the
+// feeding warps widen them to fp32 (the softplus applied once) with the tokens of a channel (of a state, for B
+// and C) contiguous, so that a lane reads four tokens with one load and pairs of tokens go through packed
+// multiply-adds, and write the results out.  A tile is widened while the one before it is worked on: one
+// barrier a tile.  Tokens past the segment's end are staged as delta = x = 0, which leaves every state as it is.
 #pragma once
 
-#include "kda_gate_math.cuh"
 #include "mix_common.cuh"
 
 namespace gdn {
 namespace mix {
 
-constexpr int kTile = 32;        // tokens of a staged tile: one a lane
-constexpr int kRow = kTile + 4;  // its padded row: 16-byte aligned quads, CW rows on distinct banks
-constexpr int kWarps = 4;        // warps of a block
-constexpr int kCkpt = 16;        // tokens between the states that the forward keeps for the backward
+constexpr int kTile = 32;        // tokens of a staged tile
+constexpr int kRow = kTile + 4;  // a widened row: rows of a warp, or of its lanes, are on distinct banks
+constexpr int kFeed = 128;       // feeding threads: a lane has a token, a warp a quarter of the channels
+// Raw tiles in flight; two where the widest tiles would not fit otherwise.
+template <typename T, int NP>
+constexpr int kRing = sizeof(T) == 4 && NP == 64 ? 2 : 3;
+constexpr int kCkpt = 16;  // tokens between the states that the forward keeps for the backward
 constexpr int kCkptLog = 4;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 
-template <int NP>
+template <int NP, int SPL>
 struct Shape {
-  static constexpr int NL = NP / 4;        // lanes of a channel
-  static constexpr int CW = 32 / NL;       // channels of a warp
-  static constexpr int CC = CW * kWarps;   // and of a block
+  static constexpr int NL = NP / SPL;       // lanes of a channel
+  static constexpr int CW = 32 / NL;        // channels of a warp
+  static constexpr int CC = 512 / NP;       // channels of a block
+  static constexpr int WORK = 32 * CC / CW; // threads that hold states; the feeding threads follow
+  static constexpr int NT = WORK + kFeed;
+  static constexpr int FC = CC / 4;         // channels of a feeding thread
 };
+
+// The row of state n in a widened [NP][kRow] array: the rows that lanes read together are neighbours.
+template <int NP, int SPL>
+__device__ __forceinline__ int state_row(int n) { return (n % SPL * (NP / SPL) + n / SPL) * kRow; }
+
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -45,14 +55,35 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// softplus with the framework's pass-through above 20
-__device__ __forceinline__ float softplus_acc(float x) {
-  return x > 20.f ? x : fmaxf(x, 0.f) + log1p_unit(exp_acc(-fabsf(x)));
+// The framework's softplus (v above 20 passes through) of two values, and e = exp(-|v|) for their slope.
+// softplus = max(v, 0) + log(1 + e).  The exponent's product is carried with its remainder, as in exp_acc;
+// log(1 + e) / e on [0, 1] is a polynomial of degree 9 (a least-squares fit of the relative error, 2^-27).
+__device__ __forceinline__ float2 softplus2(float2 v, float2& e) {
+  const float2 a = {fminf(fabsf(v.x), 100.f), fminf(fabsf(v.y), 100.f)};
+  const float2 t = __fmul2_rn(a, {-kLog2e, -kLog2e});
+  float2 r = __ffma2_rn(a, {-kLog2e, -kLog2e}, {-t.x, -t.y});
+  r = __ffma2_rn(a, {-1.92596299e-8f, -1.92596299e-8f}, r);
+  e = {ex2(t.x), ex2(t.y)};
+  e = __ffma2_rn(__fmul2_rn(e, r), {kLn2, kLn2}, e);
+  constexpr float c[10] = {1.f,          -0.499999017f, 0.333299637f, -0.249541342f, 0.196759388f,
+                           -0.153055906f, 0.106036514f,  -0.0569594987f, 0.0198514443f, -0.00324402121f};
+  float2 p = {c[9], c[9]};
+#pragma unroll
+  for (int k = 8; k >= 0; --k) p = __ffma2_rn(p, e, {c[k], c[k]});
+  // comparisons that are false for NaN leave it in the result
+  float2 o = {v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y};
+  o = __ffma2_rn(p, e, o);
+  return {v.x > 20.f ? v.x : o.x, v.y > 20.f ? v.y : o.y};
+}
+// softplus' = 1 / (1 + exp(-v)), 1 above 20
+__device__ __forceinline__ float softplus_slope(float v, float e) {
+  const float r = rcp(1.f + e);
+  return v > 20.f ? 1.f : v < 0.f ? e * r : r + (v - v);
 }
 
 // Sums M values over the lanes (lane / STRIDE) % LANES.  While a lane has several values, each step
 // halves them: a lane keeps one half and hands over the other.  Afterwards a lane has M / LANES values,
-// the first of them number M / LANES * (its index in bit-reversed order), or one that LANES / M lanes share.
+// the first of them number lane_slot, or one that LANES / M lanes share.
 template <int M, int LANES, int STRIDE>
 __device__ __forceinline__ void lane_sums(float* v, int lane) {
   if constexpr (LANES > 1) {
@@ -80,72 +111,109 @@ __device__ __forceinline__ int lane_slot(int l) {
   return at;
 }
 
-// A warp's tile of one per-channel input, as fetched: lane = token.
+// A feeding thread's share of the asynchronous copies of a [kTile][WIDTH] tile of rows with a token stride, to rows
+// of PITCH elements.  Rows of whole 16-byte words; anything else goes through registers.  What does not exist is zero.
+template <typename T, int WIDTH, int PITCH>
+struct Feed {
+  static constexpr int V = 16 / (int)sizeof(T), PER = WIDTH / V, ALL = kTile * PER, N = (ALL + kFeed - 1) / kFeed;
+  const T* base;
+  int64_t ld;
+  int width;
+  bool vec;
+
+  __device__ __forceinline__ void fetch(T* dst, int f, int64_t t0, int tokens) const {
+    if (vec) {
+      const int c = f % PER * V;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int t = i * (kFeed / PER) + f / PER;
+        if (ALL % kFeed != 0 && t >= kTile) break;
+        const bool in = t < tokens && c < width;
+        const T* src = in ? base + (t0 + t) * ld + c : base;
+        const unsigned d = (unsigned)__cvta_generic_to_shared(dst + t * PITCH + c);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(in ? 16 : 0));
+      }
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kTile * WIDTH / kFeed; ++i) {
+        const int e = i * kFeed + f, t = e / WIDTH, c = e % WIDTH;
+        const bool in = t < tokens && c < width;
+        const T* src = in ? base + (t0 + t) * ld + c : base;
+        const unsigned d = (unsigned)__cvta_generic_to_shared(dst + t * PITCH + c);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(in ? 4 : 0));
+      }
+    } else {  // half words have no asynchronous copy: all of a thread's loads are under way before the first is stored
+      constexpr int PER = kTile * WIDTH / kFeed;
+      T v[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int e = i * kFeed + f, t = e / WIDTH, c = e % WIDTH;
+        v[i] = down<T>(0.f);
+        if (t < tokens && c < width) v[i] = base[(t0 + t) * ld + c];
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int e = i * kFeed + f;
+        dst[e / WIDTH * PITCH + e % WIDTH] = v[i];
+      }
+    }
+  }
+};
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
+
+// B or C of a raw tile [kTile][NP] to fp32 [NP][kRow]: a feeding thread takes four tokens of a state.
+template <typename T, int NP, int SPL>
+__device__ __forceinline__ void widen_states(float* to, const T* raw, int f) {
+#pragma unroll
+  for (int i = 0; i < (NP * 8 + kFeed - 1) / kFeed; ++i) {
+    const int e = i * kFeed + f, n = e % NP, q = e / NP;
+    if (NP * 8 % kFeed != 0 && q >= 8) break;
+    const T* r = raw + q * 4 * NP + n;
+    *reinterpret_cast<float4*>(to + state_row<NP, SPL>(n) + 4 * q) = make_float4(up<T>(r[0]), up<T>(r[NP]), up<T>(r[2 * NP]), up<T>(r[3 * NP]));
+  }
+}
+
+// CW channels of a token in registers, as they are in memory.
 template <typename T, int CW>
 struct Cols {
   static constexpr int V = CW * (int)sizeof(T) > 16 ? 16 / (int)sizeof(T) : CW;
   Pack<T, V> r[CW / V];
 
-  // row: the token's first element of the warp's channels; n: how many of them exist
-  __device__ __forceinline__ void fetch(const T* row, bool in, bool vec, int n) {
-    if (vec) {
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-      for (int i = 0; i < CW / V; ++i) {
-        if (in && n > 0)
-          r[i].load(row + i * V);
-        else
-          r[i].zero();
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < CW; ++i) r[i / V].v[i % V] = in && i < n ? row[i] : down<T>(0.f);
-    }
+    for (int i = 0; i < CW / V; ++i) r[i].load(p + i * V);
   }
   __device__ __forceinline__ float get(int i) const { return up<T>(r[i / V].v[i % V]); }
   __device__ __forceinline__ void put(int i, float f) { r[i / V].v[i % V] = down<T>(f); }
-  __device__ __forceinline__ void store(T* row, bool in, bool vec, int n) const {
-    if (!in) return;
+  // n: how many of them exist (vec: whole vectors of them)
+  __device__ __forceinline__ void store(T* p, bool vec, int n) const {
     if (vec) {
-      if (n > 0) {
 #pragma unroll
-        for (int i = 0; i < CW / V; ++i) r[i].store(row + i * V);
-      }
+      for (int i = 0; i < CW / V; ++i)
+        if (i * V < n) r[i].store(p + i * V);
     } else {
 #pragma unroll
       for (int i = 0; i < CW; ++i)
-        if (i < n) row[i] = r[i / V].v[i % V];
+        if (i < n) p[i] = r[i / V].v[i % V];
     }
   }
 };
 
-// A block's tile of B or C: [kTile][NP] floats in shared memory, zero past N and past the piece.
-template <typename T, int NP>
-struct Mat {
-  static constexpr int PER = kTile * NP / (kWarps * 32);
-  T r[PER];
-
-  // m: element (first token of the tile, state 0)
-  __device__ __forceinline__ void fetch(const T* m, int64_t ld, int N, int tokens) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = i * kWarps * 32 + threadIdx.x, t = e / NP, n = e % NP;
-      r[i] = t < tokens && n < N ? m[t * ld + n] : down<T>(0.f);
-    }
-  }
-  __device__ __forceinline__ void stage(float* s) const {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) s[i * kWarps * 32 + threadIdx.x] = up<T>(r[i]);
-  }
-};
-
-// Where a block and a warp are: unit, group and channels.
-template <int NP>
+// Where a block and a thread are.
+template <int NP, int SPL>
 struct Place {
-  using S = Shape<NP>;
+  using S = Shape<NP, SPL>;
   Piece p;
-  int g, warp, lane, nl, cl, n;  // n: channels that exist of the warp's
-  int64_t c0, ch;                // the warp's first channel, the lane's
-  bool live;
+  int g;           // group
+  int64_t tile;    // the block's channel tile in the group
+  int lane, nl, cl, warp;
+  int c, n0;       // working threads: the lane's channel in the block and its first state
+  bool feeds, live;
+  int f, tok, sc;  // feeding threads: their number, token and first channel
+  int width;       // channels of the block that exist
+  int64_t c0, ch;  // the block's first channel, the lane's
 
   // whether the unit exists; the channels are set either way
   __device__ __forceinline__ bool find(const Ssm& s, int lg) {
@@ -153,26 +221,73 @@ struct Place {
     lane = threadIdx.x & 31;
     nl = lane % S::NL;
     cl = lane / S::NL;
+    c = warp * S::CW + cl;
+    n0 = nl * SPL;
+    feeds = threadIdx.x >= S::WORK;
+    f = (int)threadIdx.x - S::WORK;
+    tok = lane;
+    sc = (f >> 5) * S::FC;
     const int64_t Dg = s.D / s.G, tiles = (Dg + S::CC - 1) / S::CC;
     g = (int)(blockIdx.y / tiles);
-    const int64_t local = (blockIdx.y - g * tiles) * S::CC + warp * S::CW, rest = Dg - local;
-    n = rest <= 0 ? 0 : rest < S::CW ? (int)rest : S::CW;
+    tile = blockIdx.y - g * tiles;
+    const int64_t local = tile * S::CC, rest = Dg - local;
     c0 = g * Dg + local;
-    ch = c0 + cl;
-    live = cl < n;
+    ch = c0 + c;
+    live = !feeds && c < rest;
+    width = rest < S::CC ? (int)rest : S::CC;
     return find_piece(s.seqs, blockIdx.x, lg, p);
   }
 };
 
-// Four states of a lane from and to [...][D][N] and the padded [...][D][NP] workspace.
-__device__ __forceinline__ void load_states(const float* p, int N, int n0, float (&h)[4]) {
+// The block's raw tiles of one per-channel input; a row is padded so that lanes on neighbouring tokens read
+// distinct banks.
+template <typename T, int NP>
+struct RawRows {
+  static constexpr int CC = 512 / NP, PITCH = CC + 16 / (int)sizeof(T);
+  T v[kRing<T, NP>][kTile * PITCH];
+};
+
+// A block's view of the inputs of its segment.
+template <typename T, int NP, int SPL>
+struct Inputs {
+  static constexpr int CC = 512 / NP;
+  Feed<T, CC, RawRows<T, NP>::PITCH> x, dt, dy;
+  Feed<T, NP, NP> B, C;
+
+  __device__ __forceinline__ Inputs(const Ssm& s, const Place<NP, SPL>& at) {
+    const int64_t t0 = at.p.t0, n = (int64_t)at.g * s.N;
+    x = {static_cast<const T*>(s.x) + t0 * s.ld_x + at.c0, s.ld_x, at.width, s.vec};
+    dt = {static_cast<const T*>(s.dt) + t0 * s.ld_dt + at.c0, s.ld_dt, at.width, s.vec};
+    dy = {static_cast<const T*>(s.dy) + t0 * s.D + at.c0, s.D, at.width, s.vec};
+    B = {static_cast<const T*>(s.Bm) + t0 * s.ld_b + n, s.ld_b, s.N, s.vec_bc};
+    C = {static_cast<const T*>(s.Cm) + t0 * s.ld_c + n, s.ld_c, s.N, s.vec_bc};
+  }
+};
+
+// The states of a lane from and to [...][D][N] ...
+template <int SPL>
+__device__ __forceinline__ void load_states(const float* p, int N, int n0, float (&h)[SPL]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) h[j] = n0 + j < N ? p[n0 + j] : 0.f;
+  for (int j = 0; j < SPL; ++j) h[j] = n0 + j < N ? p[n0 + j] : 0.f;
 }
-__device__ __forceinline__ void store_states(float* p, int N, int n0, const float (&h)[4]) {
+template <int SPL>
+__device__ __forceinline__ void store_states(float* p, int N, int n0, const float (&h)[SPL]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < SPL; ++j)
     if (n0 + j < N) p[n0 + j] = h[j];
+}
+// ... and the workspace's padded [...][D][NP]
+template <int SPL>
+__device__ __forceinline__ void load_padded(const float* p, float (&h)[SPL]) {
+  Pack<float, SPL> v;
+  v.load(p);
+  v.get(h);
+}
+template <int SPL>
+__device__ __forceinline__ void store_padded(float* p, const float (&h)[SPL]) {
+  Pack<float, SPL> v;
+  v.set(h);
+  v.store(p);
 }
 
 // A log2(e), kept finite so that a token of delta = 0 past the piece's end keeps the state
@@ -181,15 +296,22 @@ __device__ __forceinline__ float decay_rate(float A_log) {
   return a < -3.4e38f ? -3.4e38f : a;
 }
 
-// that of a lane's four states (0 for states that do not exist: their decay is 1, their input 0)
-__device__ __forceinline__ void load_decay(const Ssm& s, int64_t ch, bool live, int n0, float (&a)[4]) {
+// that of a lane's states (0 for states that do not exist: their decay is 1, their input 0)
+template <int SPL>
+__device__ __forceinline__ void load_decay(const Ssm& s, int64_t ch, bool live, int n0, float (&a)[SPL]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) a[j] = live && n0 + j < s.N ? decay_rate(s.A_log[ch * s.N + n0 + j]) : 0.f;
+  for (int j = 0; j < SPL; ++j) a[j] = live && n0 + j < s.N ? decay_rate(s.A_log[ch * s.N + n0 + j]) : 0.f;
 }
 
 template <int NP>
 __device__ __forceinline__ int64_t state_at(const Ssm& s, int64_t unit, int64_t ch, int n0) {
   return (unit * s.D + ch) * NP + n0;
+}
+
+// A kernel's dynamic shared memory, asked for where it is over the default.
+template <typename K>
+inline cudaError_t allow_shared(K* kernel, size_t bytes) {
+  return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
 }
 
 }  // namespace mix
