@@ -60,8 +60,7 @@ cudaError_t column_sums(const char* name, const float* part, int64_t n, int64_t 
 
 namespace {
 
-constexpr int FS = 8;   // tokens of a thread's strip, forward
-constexpr int BS = 16;  // and backward
+constexpr int BS = 32;  // tokens of a thread's strip, backward
 constexpr int NT = 256;
 
 // Row p (place in the sequence, may be negative) of the sequence's inputs.
@@ -75,180 +74,304 @@ __device__ __forceinline__ void load_row(const Conv& c, const Piece& p, int at, 
     r.zero();
 }
 
-template <typename T, int V, int W>
-__device__ __forceinline__ void load_taps(const Conv& c, int64_t ch, float (&w)[W][V]) {
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-#pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = c.weight[(ch + i) * W + j];
+// The taps and the bias of the block's channels to shared memory, [W + 1][cols + 4]: read in memory order (a
+// thread's own W V taps are far from the next lane's), left with the channels next to one another.
+template <int W>
+__device__ __forceinline__ void stage_taps(const Conv& c, float* taps, int64_t c0, int cols) {
+  const int n = threadIdx.y * blockDim.x + threadIdx.x;
+  const int have = (int)min((int64_t)cols, c.D - c0);
+  for (int e = n; e < have * W; e += NT) taps[e % W * (cols + 4) + e / W] = c.weight[c0 * W + e];
+  for (int e = n; e < have; e += NT) taps[W * (cols + 4) + e] = c.bias ? c.bias[c0 + e] : 0.f;
 }
 
-// Block (lanes over channel vectors, strips of tokens); all of a strip's rows are requested before
-// the first is used.
+// Pairs of channels, for packed multiply-adds; a single channel leaves the second lane of its pair empty.
+template <int V>
+struct Pairs {
+  static constexpr int N = (V + 1) / 2;
+  float2 v[N];
+  template <typename T>
+  __device__ __forceinline__ void from(const Pack<T, V>& p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = p.pair(i);
+  }
+  template <typename T>
+  __device__ __forceinline__ void to(Pack<T, V>& p) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p.set_pair(i, v[i]);
+  }
+  __device__ __forceinline__ void load(const float* p) {
+    if constexpr (V == 1) {
+      v[0] = {p[0], 0.f};
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const float2*>(p + 2 * i);
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ float2 sigmoid2(float2 a) {
+  return {sigmoid<T>(a.x), sigmoid<T>(a.y)};
+}
+
+// A thread's own rows on their way through shared memory: two halves of kHalf rows, one under way while the other
+// is worked on.  Nobody else touches them, so they need no barrier.  Narrow elements without an asynchronous copy
+// of their size are loaded as they are asked for.
+constexpr int kHalf = 8;
+
+template <typename T, int V>
+struct Ring {
+  static constexpr int BYTES = V * (int)sizeof(T), SLOT = NT * (BYTES < 4 ? 4 : BYTES), HALF = kHalf * SLOT;
+  static constexpr size_t bytes = 2 * HALF;
+  unsigned to, from;  // this thread's first slot of the half to fill and of the half to read
+
+  __device__ __forceinline__ Ring(const char* shared, int n) {
+    from = (unsigned)__cvta_generic_to_shared(shared) + n * (SLOT / NT);
+    to = from;
+  }
+  // the next row of the half to fill, its k-th
+  __device__ __forceinline__ void ask(int k, const T* src, bool in) const {
+    if constexpr (BYTES == 16) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + k * SLOT), "l"(src), "r"(in ? 16 : 0) : "memory");
+    } else if constexpr (BYTES >= 4) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to + k * SLOT), "l"(src), "n"(BYTES), "r"(in ? BYTES : 0) : "memory");
+    } else {
+      const unsigned v = in ? *reinterpret_cast<const unsigned short*>(src) : 0u;
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + k * SLOT), "r"(v) : "memory");
+    }
+  }
+  __device__ __forceinline__ Pack<T, V> get(int k) const {
+    Pack<T, V> r;
+    const unsigned at = from + k * SLOT;
+    if constexpr (BYTES == 16)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.u[0]), "=r"(r.u[1]), "=r"(r.u[2]), "=r"(r.u[3]) : "r"(at) : "memory");
+    else if constexpr (BYTES == 8)
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.u[0]), "=r"(r.u[1]) : "r"(at) : "memory");
+    else
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r.u[0]) : "r"(at) : "memory");
+    return r;
+  }
+  // go on to the other half, to fill (`way` = HALF, -HALF in turn) or to read
+  __device__ __forceinline__ void filled(int way) { to += way; }
+  __device__ __forceinline__ void read(int way) { from += way; }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  template <int PENDING>
+  static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
+};
+
+// Block (lanes over channel vectors, strips of `strip` tokens).  The window of the last W inputs is a ring whose
+// places repeat every W tokens, so a round of GR tokens (a multiple of W) is one copy of the code.
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(NT) k_conv_fwd(Conv c, int lg) {
+__global__ void __launch_bounds__(NT, W <= 4 ? 2 : 1) k_conv_fwd(Conv c, int lg, int strip) {
+  extern __shared__ __align__(16) char shared[];
   if (bad_call(c.seqs)) return;
   Piece p;
   if (!find_piece(c.seqs, blockIdx.x, lg, p)) return;
-  const int64_t ch = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V;
-  if (ch >= c.D) return;
-  const int s0 = p.pos + threadIdx.y * FS;
-  const int end = p.pos + p.len;
-  if (s0 < end) {
-    Pack<T, V> rows[FS + W - 1];
+  const int cols = blockDim.x * V;
+  const int64_t c0 = (int64_t)blockIdx.y * cols, ch = c0 + threadIdx.x * V;
+  Ring<T, V> ring(shared, threadIdx.y * blockDim.x + threadIdx.x);
+  float* taps = reinterpret_cast<float*>(shared + Ring<T, V>::bytes);
+  const bool live = ch < c.D;
+  const int end = p.pos + p.len, s0 = p.pos + threadIdx.y * strip, s1 = live ? min(end, s0 + strip) : s0;
+  constexpr int N = Pairs<V>::N, GR = kHalf / W * W, HALF = Ring<T, V>::HALF;
+  const T* x = static_cast<const T*>(c.x) + (p.t0 - p.pos + s0) * c.ld + ch;  // the next row to ask for
+  int left = s1 - s0;
+  auto ask = [&](int way) {
 #pragma unroll
-    for (int i = 0; i < FS + W - 1; ++i) {
-      const int at = s0 + i - (W - 1);
-      if (at < end) load_row<T, V>(c, p, at, ch, rows[i]);
-    }
-    float w[W][V], bias[V];
-    load_taps<T, V, W>(c, ch, w);
+    for (int k = 0; k < GR; ++k, x += c.ld) ring.ask(k, x, k < left);
+    left -= GR;
+    ring.commit();
+    ring.filled(way);
+  };
+  ask(HALF);
+  ask(-HALF);
+  stage_taps<W>(c, taps, c0, cols);
+  __syncthreads();
+  if (s0 < s1) {
+    Pairs<V> w[W], bias;
 #pragma unroll
-    for (int i = 0; i < V; ++i) bias[i] = c.bias ? c.bias[ch + i] : 0.f;
-    T* y = static_cast<T*>(c.y) + (p.t0 - p.pos + s0) * c.D + ch;
+    for (int j = 0; j < W; ++j) w[j].load(taps + j * (cols + 4) + threadIdx.x * V);
+    bias.load(taps + W * (cols + 4) + threadIdx.x * V);
+    Pairs<V> xw[W];  // before the strip's first token, the token j - W before it is at place j
 #pragma unroll
-    for (int t = 0; t < FS; ++t) {
-      if (s0 + t >= end) break;
-      float o[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float a = bias[i];
-#pragma unroll
-        for (int j = 0; j < W; ++j) a = fmaf(w[j][i], up<T>(rows[t + j].v[i]), a);
-        o[i] = c.silu ? a * sigmoid<T>(a) : a;
-      }
+    for (int j = 0; j < W; ++j) {
       Pack<T, V> r;
-      r.set(o);
-      r.store(y + (int64_t)t * c.D);
+      if (j > 0)
+        load_row<T, V>(c, p, s0 + j - W, ch, r);
+      else
+        r.zero();
+      xw[j].from(r);
+    }
+    T* y = static_cast<T*>(c.y) + (p.t0 - p.pos + s0) * c.D + ch;
+    int way = HALF;
+#pragma unroll 1
+    for (int n = s1 - s0; n > 0; n -= GR, way = -way) {
+      ring.template wait<1>();
+#pragma unroll
+      for (int k = 0; k < GR; ++k, y += c.D) {
+        const int here = k % W;
+        xw[here].from(ring.get(k));
+        Pairs<V> o = bias;
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+          for (int i = 0; i < N; ++i) o.v[i] = __ffma2_rn(w[j].v[i], xw[(here + 1 + j) % W].v[i], o.v[i]);
+        if (c.silu) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) o.v[i] = __fmul2_rn(o.v[i], sigmoid2<T>(o.v[i]));
+        }
+        Pack<T, V> r;
+        o.to(r);
+        if (k < n) r.store(y);
+      }
+      ring.read(way);
+      ask(way);
     }
   }
-  if (c.final && end == p.slen && (int)threadIdx.y < W - 1) {
+  ring.template wait<0>();
+  if (live && c.final && end == p.slen && (int)threadIdx.y < W - 1) {
     Pack<T, V> r;
     load_row<T, V>(c, p, p.slen - (W - 1) + (int)threadIdx.y, ch, r);
     r.store(static_cast<T*>(c.final) + ((int64_t)p.seq * (W - 1) + threadIdx.y) * c.D + ch);
   }
 }
 
-// A strip slides over its tokens and the W - 1 after them: dpre of a token completes dx of the token
-// W - 1 before it.  The next four rows of x and dy are in flight while four are worked on.
+// A strip slides over its tokens and the W - 1 after them: dpre of a token completes dx of the token W - 1 before
+// it.  The windows of the last W inputs and dpre are rings whose places repeat every W tokens, so a round of GR
+// tokens (a multiple of W) is one copy of the code; the rows of the round ahead are in flight meanwhile.
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(NT) k_conv_bwd(Conv c, int lg) {
+__global__ void __launch_bounds__(NT, W <= 4 ? 2 : 1) k_conv_bwd(Conv c, int lg) {
+  extern __shared__ __align__(16) char shared[];
   __shared__ float red[NT * V];
+  constexpr int N = Pairs<V>::N, GR = kHalf / W * W, STEPS = BS + W - 1;
   if (bad_call(c.seqs)) return;
   Piece p;
   const bool some = find_piece(c.seqs, blockIdx.x, lg, p);
-  const int64_t ch = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V;
+  const int cols = blockDim.x * V;
+  const int64_t c0 = (int64_t)blockIdx.y * cols, ch = c0 + threadIdx.x * V;
   const bool live = ch < c.D;
-  float dw[W][V], db[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    db[i] = 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
-  }
+  const int me = threadIdx.y * blockDim.x + threadIdx.x;
+  Ring<T, V> xs(shared, me), gs(shared + Ring<T, V>::bytes, me);
+  float* taps = reinterpret_cast<float*>(shared + 2 * Ring<T, V>::bytes);
   const int s0 = some ? p.pos + (int)threadIdx.y * BS : 0;
-  if (some && live && (s0 < p.pos + p.len || s0 == 0)) {
-    float w[W][V], bias[V], xw[W][V], dp[W][V];
-    load_taps<T, V, W>(c, ch, w);
+  const bool busy = some && live && (s0 < p.pos + p.len || s0 == 0);
+  const int64_t bos = p.t0 - p.pos;
+  constexpr int HALF = Ring<T, V>::HALF;
+  const T* x = static_cast<const T*>(c.x) + (bos + s0) * c.ld + ch;  // the next rows to ask for
+  const T* dy = static_cast<const T*>(c.dy) + (bos + s0) * c.D + ch;
+  int left = busy ? min(STEPS, p.slen - s0) : 0;
+  auto ask = [&](int way) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      bias[i] = c.bias ? c.bias[ch + i] : 0.f;
-#pragma unroll
-      for (int j = 0; j < W; ++j) dp[j][i] = 0.f;
+    for (int k = 0; k < GR; ++k, x += c.ld, dy += c.D) {
+      xs.ask(k, x, k < left);
+      gs.ask(k, dy, k < left);
     }
+    left -= GR;
+    xs.commit();
+    xs.filled(way);
+    gs.filled(way);
+  };
+  ask(HALF);
+  ask(-HALF);
+  stage_taps<W>(c, taps, c0, cols);
+  __syncthreads();
+  Pairs<V> dw[W], db;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
+  for (int i = 0; i < N; ++i) {
+    db.v[i] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < W; ++j) dw[j].v[i] = {0.f, 0.f};
+  }
+  if (busy) {
+    Pairs<V> w[W], bias, xw[W], dp[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j].load(taps + j * (cols + 4) + threadIdx.x * V);
+    bias.load(taps + W * (cols + 4) + threadIdx.x * V);
+    // step i's values are at place i % W; before step 0, step j - W's at place j
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) dp[j].v[i] = {0.f, 0.f};
       Pack<T, V> r;
-      load_row<T, V>(c, p, s0 + j - (W - 1), ch, r);
-      r.get(xw[j + 1]);
+      if (j > 0)
+        load_row<T, V>(c, p, s0 + j - W, ch, r);
+      else
+        r.zero();
+      xw[j].from(r);
     }
-    const int64_t bos = p.t0 - p.pos;
-    const T* dy = static_cast<const T*>(c.dy) + bos * c.D + ch;
-    T* dx = static_cast<T*>(c.dx) + bos * c.D + ch;
-    constexpr int STEPS = BS + W - 1, GR = 4;
-    Pack<T, V> xb[GR], yb[GR];
-    auto fetch = [&](int i, Pack<T, V>& x, Pack<T, V>& g) {
-      const int at = s0 + i;
-      if (i < STEPS && at < p.slen) {
-        load_row<T, V>(c, p, at, ch, x);
-        g.load(dy + (int64_t)at * c.D);
-      } else {
-        x.zero();
-        g.zero();
-      }
-    };
+    T* dx = static_cast<T*>(c.dx) + (bos + s0 - (W - 1)) * c.D + ch;  // of the token that a step completes
+    int way = HALF;
+#pragma unroll 1
+    for (int i0 = 0; i0 < STEPS; i0 += GR, way = -way) {
+      xs.template wait<1>();
 #pragma unroll
-    for (int k = 0; k < GR; ++k) fetch(k, xb[k], yb[k]);
-#pragma unroll
-    for (int i0 = 0; i0 < STEPS; i0 += GR) {
-      Pack<T, V> xc[GR], yc[GR];
-#pragma unroll
-      for (int k = 0; k < GR; ++k) {
-        xc[k] = xb[k];
-        yc[k] = yb[k];
-      }
-#pragma unroll
-      for (int k = 0; k < GR; ++k) fetch(i0 + GR + k, xb[k], yb[k]);
-#pragma unroll
-      for (int k = 0; k < GR; ++k) {
-        const int i = i0 + k;
+      for (int k = 0; k < GR; ++k, dx += c.D) {
+        const int i = i0 + k, at = s0 + i;
         if (i >= STEPS) break;
-        const int at = s0 + i;
+        constexpr int L = W - 1;
+        const int here = k % W;
         const bool in = at < p.slen;
-        float xn[V], g[V];
-        xc[k].get(xn);
-        yc[k].get(g);
+        xw[here].from(xs.get(k));
+        Pairs<V> g;
+        g.from(gs.get(k));
+        if (c.silu) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
+          for (int v = 0; v < N; ++v) {
+            float2 a = bias.v[v];
 #pragma unroll
-          for (int j = 0; j < W - 1; ++j) {
-            xw[j][v] = xw[j + 1][v];
-            dp[j][v] = dp[j + 1][v];
-          }
-          xw[W - 1][v] = xn[v];
-          float d = g[v];
-          if (c.silu) {
-            float a = bias[v];
-#pragma unroll
-            for (int j = 0; j < W; ++j) a = fmaf(w[j][v], xw[j][v], a);
-            const float sg = sigmoid<T>(a);
-            d *= sg * fmaf(a, 1.f - sg, 1.f);
-          }
-          dp[W - 1][v] = in ? d : 0.f;
-          if (i < BS && in) {
-            db[v] += d;
-#pragma unroll
-            for (int j = 0; j < W; ++j) dw[j][v] = fmaf(d, xw[j][v], dw[j][v]);
+            for (int j = 0; j < W; ++j) a = __ffma2_rn(w[j].v[v], xw[(here + 1 + j) % W].v[v], a);
+            const float2 sg = sigmoid2<T>(a), one = {1.f, 1.f};
+            const float2 rest = __ffma2_rn(sg, {-1.f, -1.f}, one);
+            g.v[v] = __fmul2_rn(g.v[v], __fmul2_rn(sg, __ffma2_rn(a, rest, one)));
           }
         }
-        const int q = at - (W - 1);  // the token whose gradient is now complete
-        const bool own = i >= W - 1 && q < p.slen;
+#pragma unroll
+        for (int v = 0; v < N; ++v) {
+          if (!in) g.v[v] = {0.f, 0.f};
+          dp[here].v[v] = g.v[v];
+        }
+        if (i < BS && in) {
+#pragma unroll
+          for (int v = 0; v < N; ++v) {
+            db.v[v] = __fadd2_rn(db.v[v], g.v[v]);
+#pragma unroll
+            for (int j = 0; j < W; ++j) dw[j].v[v] = __ffma2_rn(g.v[v], xw[(here + 1 + j) % W].v[v], dw[j].v[v]);
+          }
+        }
+        const int q = at - L;  // the token whose gradient is now complete
+        const bool own = i >= L && q < p.slen;
         const bool before = q < 0 && s0 == 0;
         if ((own || before) && (own ? c.dx != nullptr : c.dinit != nullptr)) {
-          float o[V];
+          Pairs<V> o;
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            o[v] = 0.f;
+          for (int v = 0; v < N; ++v) {
+            o.v[v] = __fmul2_rn(w[L].v[v], dp[(here + 1) % W].v[v]);
 #pragma unroll
-            for (int j = 0; j < W; ++j) o[v] = fmaf(w[j][v], dp[W - 1 - j][v], o[v]);
+            for (int j = 1; j < W; ++j) o.v[v] = __ffma2_rn(w[L - j].v[v], dp[(here + 1 + j) % W].v[v], o.v[v]);
           }
-          const int slot = q - p.slen + (W - 1);  // its place in the final state
+          const int slot = q - p.slen + L;  // its place in the final state
           if (c.dfinal && slot >= 0) {
             Pack<T, V> r;
-            r.load(static_cast<const T*>(c.dfinal) + ((int64_t)p.seq * (W - 1) + slot) * c.D + ch);
+            r.load(static_cast<const T*>(c.dfinal) + ((int64_t)p.seq * L + slot) * c.D + ch);
+            Pairs<V> f;
+            f.from(r);
 #pragma unroll
-            for (int v = 0; v < V; ++v) o[v] += up<T>(r.v[v]);
+            for (int v = 0; v < N; ++v) o.v[v] = __fadd2_rn(o.v[v], f.v[v]);
           }
           Pack<T, V> r;
-          r.set(o);
+          o.to(r);
           if (own)
-            r.store(dx + (int64_t)q * c.D);
+            r.store(dx);
           else
-            r.store(static_cast<T*>(c.dinit) + ((int64_t)p.seq * (W - 1) + i) * c.D + ch);
+            r.store(static_cast<T*>(c.dinit) + ((int64_t)p.seq * L + i) * c.D + ch);
         }
       }
+      xs.read(way);
+      gs.read(way);
+      ask(way);
     }
   }
+  xs.template wait<0>();
   if (!c.part) return;
   // the block's strips in order, one tap at a time
   float* part = c.part + (int64_t)blockIdx.x * (W + 1) * c.D + ch;
@@ -256,7 +379,10 @@ __global__ void __launch_bounds__(NT) k_conv_bwd(Conv c, int lg) {
   for (int j = 0; j <= W; ++j) {
     __syncthreads();
 #pragma unroll
-    for (int v = 0; v < V; ++v) red[(threadIdx.y * blockDim.x + threadIdx.x) * V + v] = j < W ? dw[j < W ? j : 0][v] : db[v];
+    for (int v = 0; v < V; ++v) {
+      const float2 f = j < W ? dw[j < W ? j : 0].v[v / 2] : db.v[v / 2];
+      red[(threadIdx.y * blockDim.x + threadIdx.x) * V + v] = v % 2 ? f.y : f.x;
+    }
     __syncthreads();
     if (threadIdx.y == 0 && live) {
 #pragma unroll
@@ -281,13 +407,12 @@ __global__ void __launch_bounds__(NT) k_conv_step(Conv c) {
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) rows[j].load(st + (int64_t)j * c.D);
   rows[W - 1].load(static_cast<const T*>(c.x) + n * c.ld + ch);
-  float w[W][V], o[V];
-  load_taps<T, V, W>(c, ch, w);
+  float o[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     float a = c.bias ? c.bias[ch + i] : 0.f;
 #pragma unroll
-    for (int j = 0; j < W; ++j) a = fmaf(w[j][i], up<T>(rows[j].v[i]), a);
+    for (int j = 0; j < W; ++j) a = fmaf(c.weight[(ch + i) * W + j], rows[j].f(i), a);
     o[i] = c.silu ? a * sigmoid<T>(a) : a;
   }
   Pack<T, V> r;
@@ -325,11 +450,20 @@ bool vec_ok(const Conv& c, int es, int V) {
 // that the partial rows' count is a function of the sizes alone.
 int bwd_lg(int64_t D) { return log2i(BS * NT / lanes_of(D, 4)); }
 
+size_t taps_bytes(int lanes, int V, int W) { return (size_t)(W + 1) * (lanes * V + 4) * sizeof(float); }
+
 template <typename T, int V, int W>
 cudaError_t fwd_w(const Conv& c, cudaStream_t s) {
-  const int lanes = lanes_of(c.D, V), lg = log2i(FS * NT / lanes);
-  const dim3 grid((unsigned)max_units(c.seqs, lg), (unsigned)((c.D + (int64_t)lanes * V - 1) / ((int64_t)lanes * V)));
-  k_conv_fwd<T, V, W><<<grid, dim3(lanes, NT / lanes), 0, s>>>(c, lg);
+  const int lanes = lanes_of(c.D, V);
+  const int64_t across = (c.D + (int64_t)lanes * V - 1) / ((int64_t)lanes * V);
+  int strip = kHalf, lg = log2i(strip * NT / lanes);
+  // strips of up to 64 tokens while eight blocks for each of 148 multiprocessors are left
+  const int64_t tokens = c.seqs.cu ? c.seqs.T : c.seqs.T * c.seqs.n;
+  while (strip < 64 && (tokens >> (lg + 1)) * across >= 148 * 8) strip *= 2, ++lg;
+  const dim3 grid((unsigned)max_units(c.seqs, lg), (unsigned)across);
+  const size_t bytes = Ring<T, V>::bytes + taps_bytes(lanes, V, W);
+  if (cudaError_t e = allow_shared(k_conv_fwd<T, V, W>, bytes)) return e;
+  k_conv_fwd<T, V, W><<<grid, dim3(lanes, NT / lanes), bytes, s>>>(c, lg, strip);
   return cudaGetLastError();
 }
 
@@ -337,7 +471,9 @@ template <typename T, int V, int W>
 cudaError_t bwd_w(const Conv& c, cudaStream_t s) {
   const int lanes = lanes_of(c.D, 4), lg = bwd_lg(c.D);
   const dim3 grid((unsigned)max_units(c.seqs, lg), (unsigned)((c.D + (int64_t)lanes * V - 1) / ((int64_t)lanes * V)));
-  k_conv_bwd<T, V, W><<<grid, dim3(lanes, NT / lanes), 0, s>>>(c, lg);
+  const size_t bytes = 2 * Ring<T, V>::bytes + taps_bytes(lanes, V, W);
+  if (cudaError_t e = allow_shared(k_conv_bwd<T, V, W>, bytes)) return e;
+  k_conv_bwd<T, V, W><<<grid, dim3(lanes, NT / lanes), bytes, s>>>(c, lg);
   return cudaGetLastError();
 }
 

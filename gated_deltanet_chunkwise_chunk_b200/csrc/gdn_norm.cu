@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : NG) k_norm_fwd(Norm c, int lanes
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int v = 0; v < V; ++v) s[0] += up<T>(xr[i].v[v]);
+        for (int v = 0; v < V; ++v) s[0] += xr[i].f(v);
       row_sum<1, BLOCK>(s, lanes, sh[flip][0]);
       mu = s[0] * inv;
     }
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : NG) k_norm_fwd(Norm c, int lanes
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float d = up<T>(xr[i].v[v]) - mu;
+        const float d = xr[i].f(v) - mu;
         if (live[i]) q[0] = fmaf(d, d, q[0]);
       }
     row_sum<1, BLOCK>(q, lanes, sh[flip][1]);
@@ -130,9 +130,9 @@ __global__ void __launch_bounds__(BLOCK ? 512 : NG) k_norm_fwd(Norm c, int lanes
       float o[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        o[v] = fmaf((up<T>(xr[i].v[v]) - mu) * rstd, w[i][v], b[i][v]);
+        o[v] = fmaf((xr[i].f(v) - mu) * rstd, w[i][v], b[i][v]);
         if (z) {
-          const float g = up<T>(zr[i].v[v]);
+          const float g = zr[i].f(v);
           o[v] *= g * sigmoid<T>(g);
         }
       }
@@ -201,10 +201,10 @@ __global__ void __launch_bounds__(BLOCK ? 512 : NG) k_norm_bwd(Norm c, int lanes
       float dz[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float h = live[i] ? (up<T>(xr[i].v[v]) - m) * rs : 0.f;
-        float dn = up<T>(gr[i].v[v]);
+        const float h = live[i] ? (xr[i].f(v) - m) * rs : 0.f;
+        float dn = gr[i].f(v);
         if (z) {
-          const float g = up<T>(zr[i].v[v]), sg = sigmoid<T>(g), n = fmaf(h, w[i][v], b[i][v]);
+          const float g = zr[i].f(v), sg = sigmoid<T>(g), n = fmaf(h, w[i][v], b[i][v]);
           dz[v] = dn * n * sg * fmaf(g, 1.f - sg, 1.f);
           dn *= g * sg;
         }

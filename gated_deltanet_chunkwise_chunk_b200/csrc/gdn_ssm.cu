@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(Shape<NP, kFwd>::NT, 3) k_ssm_fwd(Ssm s) {
       const float* x = m.x[buf] + at.sc * kRow + at.tok;
       Cols<T, FC> o;
 #pragma unroll
-      for (int i = 0; i < FC; ++i) o.put(i, x[i * kRow]);
+      for (int i = 0; i < FC; i += 2) o.put2(i, {x[i * kRow], x[(i + 1) * kRow]});
       if (tile * kTile + at.tok < p.len) o.store(y + (int64_t)tile * kTile * s.D, s.vec, at.width - at.sc);
     };
     // The feeding warps meet on a barrier of their own before they widen what all of them fetched.

@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
         Cols<T, FC> ox, od;
         const bool here = t0 + at.tok < p.len;
 #pragma unroll
-        for (int k = 0; k < FC; ++k) {
-          ox.put(k, m.x[buf][from + k * kRow]);
-          od.put(k, m.d[buf][from + k * kRow]);
+        for (int k = 0; k < FC; k += 2) {
+          ox.put2(k, {m.x[buf][from + k * kRow], m.x[buf][from + (k + 1) * kRow]});
+          od.put2(k, {m.d[buf][from + k * kRow], m.d[buf][from + (k + 1) * kRow]});
         }
         if (here) {
           ox.store(dx + (int64_t)t0 * s.D, s.vec, at.width - at.sc);

@@ -47,28 +47,71 @@ struct Word<8> { using type = uint2; };
 template <>
 struct Word<16> { using type = uint4; };
 
+// Two neighbouring elements of a 16-bit type, from and to the word that holds them.
+__device__ __forceinline__ float2 widen2(unsigned w, __nv_bfloat16) {
+  return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)};
+}
+__device__ __forceinline__ float2 widen2(unsigned w, __half) {
+  __half2 h;
+  *reinterpret_cast<unsigned*>(&h) = w;
+  return __half22float2(h);
+}
+__device__ __forceinline__ unsigned narrow2(float2 f, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const unsigned*>(&h);
+}
+__device__ __forceinline__ unsigned narrow2(float2 f, __half) {
+  const __half2 h = __floats2half2_rn(f.x, f.y);
+  return *reinterpret_cast<const unsigned*>(&h);
+}
+
 template <typename T, int V>
 struct Pack {
   using W = typename Word<sizeof(T) * V>::type;
+  static constexpr int WORDS = (int)sizeof(T) * V / 4;  // 0: a single half word
   union {
     W w;
-    T v[V];
+    unsigned u[WORDS > 0 ? WORDS : 1];
+    T one;
   };
   __device__ __forceinline__ Pack() {}
   __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const W*>(p); }
   __device__ __forceinline__ void load_once(const T* p) { w = __ldcs(reinterpret_cast<const W*>(p)); }
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = down<T>(0.f);
+    for (int i = 0; i < (WORDS > 0 ? WORDS : 1); ++i) u[i] = 0u;
   }
   __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<W*>(p) = w; }
-  __device__ __forceinline__ void get(float (&f)[V]) const {
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = up<T>(v[i]);
+  // elements 2 i and 2 i + 1 (V = 1: the element and 0)
+  __device__ __forceinline__ float2 pair(int i) const {
+    if constexpr (V == 1)
+      return {up<T>(one), 0.f};
+    else if constexpr (sizeof(T) == 4)
+      return {__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])};
+    else
+      return widen2(u[i], T{});
   }
-  __device__ __forceinline__ void set(const float (&f)[V]) {
+  __device__ __forceinline__ void set_pair(int i, float2 f) {
+    if constexpr (V == 1) {
+      one = down<T>(f.x);
+    } else if constexpr (sizeof(T) == 4) {
+      u[2 * i] = __float_as_uint(f.x);
+      u[2 * i + 1] = __float_as_uint(f.y);
+    } else {
+      u[i] = narrow2(f, T{});
+    }
+  }
+  __device__ __forceinline__ float f(int i) const {
+    const float2 v = pair(i / 2);
+    return i % 2 ? v.y : v.x;
+  }
+  __device__ __forceinline__ void get(float (&o)[V]) const {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = down<T>(f[i]);
+    for (int i = 0; i < V; ++i) o[i] = f(i);
+  }
+  __device__ __forceinline__ void set(const float (&o)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) set_pair(i / 2, {o[i], i + 1 < V ? o[i + 1 < V ? i + 1 : 0] : 0.f});
   }
 };
 
@@ -97,7 +140,10 @@ __device__ __forceinline__ float rcp(float x) {
 // the remainder is enough: its relative error (2 + 1.2 |x|) 2^-23 is far below the result's rounding.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float x) {
-  return rcp(1.f + (sizeof(T) == 4 ? exp_acc(-x) : __expf(-x)));
+  if constexpr (sizeof(T) == 4) return rcp(1.f + exp_acc(-x));
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504088896341f));
+  return rcp(1.f + e);
 }
 
 // A piece of one sequence: `len` tokens from flat token `t0`, which is token `pos` of sequence `seq`
@@ -193,6 +239,12 @@ __device__ __forceinline__ float strand_sums(const float* __restrict__ part, int
     if (strand != 0 || c >= width) c = -1;
     return v;
   }
+}
+
+// A kernel's dynamic shared memory, asked for where it is over the default.
+template <typename K>
+inline cudaError_t allow_shared(K* kernel, size_t bytes) {
+  return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
 }
 
 }  // namespace mix

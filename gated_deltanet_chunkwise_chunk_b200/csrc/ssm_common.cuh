@@ -185,8 +185,16 @@ struct Cols {
 #pragma unroll
     for (int i = 0; i < CW / V; ++i) r[i].load(p + i * V);
   }
-  __device__ __forceinline__ float get(int i) const { return up<T>(r[i / V].v[i % V]); }
-  __device__ __forceinline__ void put(int i, float f) { r[i / V].v[i % V] = down<T>(f); }
+  __device__ __forceinline__ float get(int i) const { return r[i / V].f(i % V); }
+  // elements i and i + 1, i even
+  __device__ __forceinline__ void put2(int i, float2 f) {
+    if constexpr (V == 1) {
+      r[i].set_pair(0, {f.x, 0.f});
+      r[i + 1].set_pair(0, {f.y, 0.f});
+    } else {
+      r[i / V].set_pair(i % V / 2, f);
+    }
+  }
   // n: how many of them exist (vec: whole vectors of them)
   __device__ __forceinline__ void store(T* p, bool vec, int n) const {
     if (vec) {
@@ -196,7 +204,7 @@ struct Cols {
     } else {
 #pragma unroll
       for (int i = 0; i < CW; ++i)
-        if (i < n) p[i] = r[i / V].v[i % V];
+        if (i < n) p[i] = reinterpret_cast<const T*>(&r[i / V])[i % V];
     }
   }
 };
@@ -306,12 +314,6 @@ __device__ __forceinline__ void load_decay(const Ssm& s, int64_t ch, bool live, 
 template <int NP>
 __device__ __forceinline__ int64_t state_at(const Ssm& s, int64_t unit, int64_t ch, int n0) {
   return (unit * s.D + ch) * NP + n0;
-}
-
-// A kernel's dynamic shared memory, asked for where it is over the default.
-template <typename K>
-inline cudaError_t allow_shared(K* kernel, size_t bytes) {
-  return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
 }
 
 }  // namespace mix
