@@ -395,7 +395,8 @@ __global__ void __launch_bounds__(NT, W <= 4 ? 2 : 1) k_conv_bwd(Conv c, int lg)
   }
 }
 
-// One token for each sequence; the state moves up by one input.  state and final may be one buffer:
+// One token for each sequence, two channels to a thread (more would put a thread's taps far from the next
+// lane's); the state moves up by one input.  state and final may be one buffer:
 // a thread reads its channels' slots before it writes them.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(NT) k_conv_step(Conv c) {
@@ -407,12 +408,22 @@ __global__ void __launch_bounds__(NT) k_conv_step(Conv c) {
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) rows[j].load(st + (int64_t)j * c.D);
   rows[W - 1].load(static_cast<const T*>(c.x) + n * c.ld + ch);
-  float o[V];
+  float o[V], w[V * W];
+  if constexpr (V * W % 4 == 0) {  // (ch is a multiple of V)
+#pragma unroll
+    for (int i = 0; i < V * W; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(c.weight + ch * W + i);
+      w[i] = f.x, w[i + 1] = f.y, w[i + 2] = f.z, w[i + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V * W; ++i) w[i] = c.weight[ch * W + i];
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     float a = c.bias ? c.bias[ch + i] : 0.f;
 #pragma unroll
-    for (int j = 0; j < W; ++j) a = fmaf(c.weight[(ch + i) * W + j], rows[j].f(i), a);
+    for (int j = 0; j < W; ++j) a = fmaf(w[i * W + j], rows[j].f(i), a);
     o[i] = c.silu ? a * sigmoid<T>(a) : a;
   }
   Pack<T, V> r;
@@ -493,7 +504,7 @@ cudaError_t by_width(const Conv& c, cudaStream_t s) {
   case w:                                                    \
     return WHAT == FWD   ? fwd_w<T, V, w>(c, s)              \
            : WHAT == BWD ? bwd_w<T, (V > 4 ? 4 : V), w>(c, s) \
-                         : step_w<T, V, w>(c, s);
+                         : step_w<T, (V > 2 ? 2 : V), w>(c, s);
     GDN_CONV_W(1)
     GDN_CONV_W(2)
     GDN_CONV_W(3)

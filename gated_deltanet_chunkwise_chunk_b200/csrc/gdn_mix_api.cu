@@ -415,7 +415,10 @@ int gdn_ssm_step(const gdn_ssm_dims* d, const void* x, const void* dt, const flo
   c.init = state;
   c.y = y;
   c.final = final_state;
-  c.vec = d->S == ssm_padded((int)d->S);
+  // a state's four floats as 16 bytes; four values of B and C as one word
+  c.vec = d->S % 4 == 0;
+  const size_t w = 4 * es;
+  c.vec_bc = d->S % 4 == 0 && c.ld_b % 4 == 0 && c.ld_c % 4 == 0 && !misaligned(Bm, w) && !misaligned(Cm, w);
   return status_of(ssm_step(c, static_cast<cudaStream_t>(stream)));
 }
 

@@ -58,10 +58,60 @@ __device__ __forceinline__ int64_t row_at(int64_t r, int64_t inner, int64_t ld, 
   return o * ld + (r - o * inner) * D;
 }
 
+// A thread's own vectors of the rows to come, DEEP rows ahead, on their way through shared memory (nobody else
+// touches them, so they need no barrier).  ARR tensors of NV vectors, and a row's statistics.  DEEP: four, or as
+// many as leave room for a second block.
+template <typename T, int V, int NV, int ARR, int MOST>
+struct Ahead {
+  static constexpr int BYTES = V * (int)sizeof(T), WIDTH = BYTES < 4 ? 4 : BYTES, ROW = ARR * NV * WIDTH + 8;
+  static constexpr int FIT = 104 * 1024 / (ROW * MOST), DEEP = FIT < 2 ? 2 : FIT > 4 ? 4 : FIT;
+  static constexpr size_t bytes(int threads) { return (size_t)DEEP * ROW * threads; }
+  unsigned base;
+  int threads;
+
+  __device__ __forceinline__ Ahead(const char* shared) : base((unsigned)__cvta_generic_to_shared(shared)), threads(blockDim.x) {}
+  // thread-interleaved: vector v of a slot at [slot][v][thread], the statistics behind them
+  __device__ __forceinline__ unsigned at(int slot, int v) const {
+    return base + slot * ROW * threads + (v * threads + threadIdx.x) * WIDTH;
+  }
+  __device__ __forceinline__ unsigned stat_at(int slot) const { return base + (slot * ROW + ARR * NV * WIDTH) * threads + threadIdx.x * 8; }
+  __device__ __forceinline__ void ask(int slot, int v, const T* src, bool in) const {
+    if constexpr (BYTES == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(slot, v)), "l"(src), "r"(in ? 16 : 0) : "memory");
+    else if constexpr (BYTES >= 4)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at(slot, v)), "l"(src), "n"(BYTES), "r"(in ? BYTES : 0) : "memory");
+    else
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(at(slot, v)), "r"(in ? (unsigned)*reinterpret_cast<const unsigned short*>(src) : 0u) : "memory");
+  }
+  __device__ __forceinline__ void ask_stats(int slot, const float* src, bool in) const {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(stat_at(slot)), "l"(src), "r"(in ? 8 : 0) : "memory");
+  }
+  __device__ __forceinline__ Pack<T, V> get(int slot, int v) const {
+    Pack<T, V> r;
+    const unsigned a = at(slot, v);
+    if constexpr (BYTES == 16)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.u[0]), "=r"(r.u[1]), "=r"(r.u[2]), "=r"(r.u[3]) : "r"(a) : "memory");
+    else
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r.u[0]) : "r"(a) : "memory");
+    return r;
+  }
+  __device__ __forceinline__ float2 stats(int slot) const {
+    float2 f;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f.x), "=f"(f.y) : "r"(stat_at(slot)) : "memory");
+    return f;
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  template <int PENDING>
+  static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
+};
+
 // lanes: threads of a row; BLOCK: the whole block, else a power of two up to 32.
 template <typename T, int V, int NV, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? 512 : NG) k_norm_fwd(Norm c, int lanes) {
+  extern __shared__ __align__(16) char shared[];
   __shared__ float sh[2][2][32];
+  using A = Ahead<T, V, NV, 2, BLOCK ? 512 : NG>;
+  const A ahead(shared);
   const int lane = BLOCK ? threadIdx.x : threadIdx.x & (lanes - 1);
   const int rpb = BLOCK ? 1 : NG / lanes;
   const int64_t step = (int64_t)gridDim.x * rpb;
@@ -83,21 +133,33 @@ __global__ void __launch_bounds__(BLOCK ? 512 : NG) k_norm_fwd(Norm c, int lanes
       b[i][v] = live[i] && c.bias ? c.bias[col[i] + v] : 0.f;
     }
   }
-  int flip = 0;
+  auto ask = [&](int64_t r, int slot) {
+    const bool row = r < c.rows;
+    const T* xa = x + (row ? row_at(r, c.inner_x, c.ld_x, c.D) : 0);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) ahead.ask(slot, i, xa + col[i], row && live[i]);
+    if (z) {
+      const T* za = z + (row ? row_at(r, c.inner_z, c.ld_z, c.D) : 0);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) ahead.ask(slot, NV + i, za + col[i], row && live[i]);
+    }
+    ahead.commit();
+  };
+#pragma unroll
+  for (int k = 0; k < A::DEEP; ++k) ask(first + k * step, k);
+  int flip = 0, slot = 0;
   // every thread of a warp runs the same number of rounds (the butterflies need them all)
   for (int64_t base = (int64_t)blockIdx.x * rpb, r = first; base < c.rows; base += step, r += step) {
     const bool row = r < c.rows;
     Pack<T, V> xr[NV], zr[NV];
-    const int64_t xa = row ? row_at(r, c.inner_x, c.ld_x, c.D) : 0;
-    const int64_t za = row && z ? row_at(r, c.inner_z, c.ld_z, c.D) : 0;
+    ahead.template wait<A::DEEP - 1>();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      xr[i].zero();
-      if (row && live[i]) {
-        xr[i].load_once(x + xa + col[i]);
-        if (z) zr[i].load_once(z + za + col[i]);
-      }
+      xr[i] = ahead.get(slot, i);
+      if (z) zr[i] = ahead.get(slot, NV + i);
     }
+    ask(r + A::DEEP * step, slot);
+    slot = slot == A::DEEP - 1 ? 0 : slot + 1;
     float mu = 0.f;
     if (!c.rms) {
       float s[1] = {0.f};
@@ -145,8 +207,11 @@ __global__ void __launch_bounds__(BLOCK ? 512 : NG) k_norm_fwd(Norm c, int lanes
 
 template <typename T, int V, int NV, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? 512 : NG) k_norm_bwd(Norm c, int lanes) {
+  extern __shared__ __align__(16) char shared[];
   __shared__ float sh[2][2][32];
   __shared__ float red[BLOCK ? 1 : NG * V];
+  using A = Ahead<T, V, NV, 3, BLOCK ? 512 : NG>;
+  const A ahead(shared);
   const int lane = BLOCK ? threadIdx.x : threadIdx.x & (lanes - 1);
   const int rpb = BLOCK ? 1 : NG / lanes;
   const int64_t step = (int64_t)gridDim.x * rpb;
@@ -168,32 +233,41 @@ __global__ void __launch_bounds__(BLOCK ? 512 : NG) k_norm_bwd(Norm c, int lanes
       dw[i][v] = db[i][v] = 0.f;
     }
   }
-  Pack<T, V> xr[NV], zr[NV], gr[NV];
-  float mu = 0.f, rstd = 0.f;
-  auto fetch = [&](int64_t r) {
+  auto ask = [&](int64_t r, int slot) {
     const bool row = r < c.rows;
-    const int64_t xa = row ? row_at(r, c.inner_x, c.ld_x, c.D) : 0;
-    const int64_t za = row && z ? row_at(r, c.inner_z, c.ld_z, c.D) : 0;
+    const T* xa = x + (row ? row_at(r, c.inner_x, c.ld_x, c.D) : 0);
+    const T* ga = dy + (row ? r * c.D : 0);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      xr[i].zero();
-      gr[i].zero();
-      zr[i].zero();
-      if (row && live[i]) {
-        xr[i].load_once(x + xa + col[i]);
-        gr[i].load_once(dy + r * c.D + col[i]);
-        if (z) zr[i].load_once(z + za + col[i]);
-      }
+      ahead.ask(slot, i, xa + col[i], row && live[i]);
+      ahead.ask(slot, NV + i, ga + col[i], row && live[i]);
     }
-    mu = row ? c.stats[2 * r] : 0.f;
-    rstd = row ? c.stats[2 * r + 1] : 0.f;
+    if (z) {
+      const T* za = z + (row ? row_at(r, c.inner_z, c.ld_z, c.D) : 0);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) ahead.ask(slot, 2 * NV + i, za + col[i], row && live[i]);
+    }
+    ahead.ask_stats(slot, c.stats + (row ? 2 * r : 0), row);
+    ahead.commit();
   };
   int64_t r = (int64_t)blockIdx.x * rpb + (BLOCK ? 0 : threadIdx.x / lanes);
-  if ((int64_t)blockIdx.x * rpb < c.rows) fetch(r);
-  int flip = 0;
+#pragma unroll
+  for (int k = 0; k < A::DEEP; ++k) ask(r + k * step, k);
+  int flip = 0, slot = 0;
   for (int64_t base = (int64_t)blockIdx.x * rpb; base < c.rows; base += step, r += step) {
     const bool row = r < c.rows;
-    const float m = mu, rs = rstd;
+    Pack<T, V> xr[NV], zr[NV], gr[NV];
+    ahead.template wait<A::DEEP - 1>();
+    const float2 st = ahead.stats(slot);
+    const float m = st.x, rs = st.y;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      xr[i] = ahead.get(slot, i);
+      gr[i] = ahead.get(slot, NV + i);
+      if (z) zr[i] = ahead.get(slot, 2 * NV + i);
+    }
+    ask(r + A::DEEP * step, slot);
+    slot = slot == A::DEEP - 1 ? 0 : slot + 1;
     float xh[NV][V], u[NV][V];
     float s[2] = {0.f, 0.f};
 #pragma unroll
@@ -223,7 +297,6 @@ __global__ void __launch_bounds__(BLOCK ? 512 : NG) k_norm_bwd(Norm c, int lanes
         out.store(static_cast<T*>(c.dgate) + r * c.D + col[i]);
       }
     }
-    fetch(r + step);
     row_sum<2, BLOCK>(s, lanes, sh[flip][0]);
     flip ^= 1;
     if (!row) continue;
@@ -369,31 +442,37 @@ struct Plan {
   int64_t blocks;
 };
 
-// The backward's blocks walk over rows: four resident blocks of 256 threads on each of 148
-// multiprocessors, or two of 512.
+// The backward's blocks walk over rows: up to four of 128 threads or so on each of 148 multiprocessors.
 constexpr int64_t kBwdBlocks = 592;
+constexpr int64_t kManyRows = 148 * 8;
 
-Plan make_plan(int64_t rows, int64_t D, int V, bool bwd) {
+// Vectors of a row that a thread may hold: 64 bytes' worth in flight, backward 16 elements in registers.
+constexpr int most_vectors(int V, int es, bool bwd) { return bwd ? 16 / V : 64 / (V * es < 4 ? 4 : V * es); }
+
+Plan make_plan(int64_t rows, int64_t D, int V, int es, bool bwd) {
   Plan p{};
   const int64_t vecs = (D + V - 1) / V;
-  const int most = (bwd ? 16 : 32) / V;  // elements of a row that a thread may hold, in vectors
+  const int most = most_vectors(V, es, bwd);
   p.wide = vecs > 512 * (int64_t)most;
-  p.block = D > 512;
-  p.nv = 1;
   if (p.wide) {
     p.threads = 1024;
     p.blocks = std::min(rows, bwd ? kBwdBlocks / 2 : (int64_t)148 * 2);
     return p;
   }
+  // Many rows: as many vectors to a thread as it may hold, since a row's sums cost each of its threads the same,
+  // while 16 lanes are left to read neighbouring vectors together.
+  // Few: as many threads to a row as there are, since only its latency counts.
+  p.nv = 1;
+  while (p.nv < most && (rows >= kManyRows ? p.nv * 32 <= vecs : (vecs + p.nv - 1) / p.nv > 512)) p.nv *= 2;
+  const int64_t threads = (vecs + p.nv - 1) / p.nv;
+  p.block = threads > 32;
   if (p.block) {
-    while ((vecs + p.nv - 1) / p.nv > 512) p.nv *= 2;
-    p.threads = (int)(((vecs + p.nv - 1) / p.nv + 31) / 32 * 32);
-    p.blocks = std::min<int64_t>(rows, bwd ? kBwdBlocks * 256 / std::max(256, p.threads) : 148 * (2048 / p.threads));
+    p.threads = (int)((threads + 31) / 32 * 32);
+    p.blocks = std::min<int64_t>(rows, bwd ? kBwdBlocks * 128 / std::max(128, p.threads) : 148 * std::max(2, 512 / p.threads));
     return p;
   }
-  while ((vecs + p.nv - 1) / p.nv > 32) p.nv *= 2;
   p.threads = 1;
-  while ((int64_t)p.threads * p.nv < vecs) p.threads *= 2;
+  while (p.threads < threads) p.threads *= 2;
   const int rpb = NG / p.threads;
   p.blocks = std::min((rows + rpb - 1) / rpb, bwd ? kBwdBlocks : (int64_t)148 * 8);
   return p;
@@ -401,22 +480,26 @@ Plan make_plan(int64_t rows, int64_t D, int V, bool bwd) {
 
 template <typename T, int V, int NV, bool BWD>
 cudaError_t launch_nv(const Norm& c, const Plan& p, cudaStream_t s) {
-  if constexpr (V * NV <= (BWD ? 16 : 32)) {
-    const unsigned n = (unsigned)p.blocks;
+  if constexpr (NV <= most_vectors(V, sizeof(T), BWD)) {
+    const unsigned n = (unsigned)p.blocks, threads = p.block ? p.threads : NG;
+    constexpr int ARR = BWD ? 3 : 2;
+    const size_t bytes = p.block ? Ahead<T, V, NV, ARR, 512>::bytes(threads) : Ahead<T, V, NV, ARR, NG>::bytes(threads);
+    auto go = [&](auto* kernel) -> cudaError_t {
+      if (cudaError_t e = allow_shared(kernel, bytes)) return e;
+      kernel<<<n, threads, bytes, s>>>(c, p.threads);
+      return cudaGetLastError();
+    };
     if constexpr (BWD)
-      p.block ? k_norm_bwd<T, V, NV, true><<<n, p.threads, 0, s>>>(c, p.threads)
-              : k_norm_bwd<T, V, NV, false><<<n, NG, 0, s>>>(c, p.threads);
+      return p.block ? go(k_norm_bwd<T, V, NV, true>) : go(k_norm_bwd<T, V, NV, false>);
     else
-      p.block ? k_norm_fwd<T, V, NV, true><<<n, p.threads, 0, s>>>(c, p.threads)
-              : k_norm_fwd<T, V, NV, false><<<n, NG, 0, s>>>(c, p.threads);
-    return cudaGetLastError();
+      return p.block ? go(k_norm_fwd<T, V, NV, true>) : go(k_norm_fwd<T, V, NV, false>);
   }
   return cudaErrorInvalidValue;
 }
 
 template <typename T, int V, bool BWD>
 cudaError_t launch(const Norm& c, cudaStream_t s, int64_t* blocks) {
-  const Plan p = make_plan(c.rows, c.D, V, BWD);
+  const Plan p = make_plan(c.rows, c.D, V, sizeof(T), BWD);
   *blocks = p.blocks;
   if (p.wide) {
     if constexpr (BWD)
@@ -430,8 +513,7 @@ cudaError_t launch(const Norm& c, cudaStream_t s, int64_t* blocks) {
     case 2: return launch_nv<T, V, 2, BWD>(c, p, s);
     case 4: return launch_nv<T, V, 4, BWD>(c, p, s);
     case 8: return launch_nv<T, V, 8, BWD>(c, p, s);
-    case 16: return launch_nv<T, V, 16, BWD>(c, p, s);
-    default: return launch_nv<T, V, 32, BWD>(c, p, s);
+    default: return launch_nv<T, V, 16, BWD>(c, p, s);
   }
 }
 

@@ -212,51 +212,95 @@ __global__ void __launch_bounds__(256) k_ssm_join(Ssm s) {
   }
 }
 
-// One token for each sequence: a thread has four states of a channel, so a state moves as 16 bytes.
-// init and final may be one buffer: a thread reads its states before it writes them.
+// One token for each sequence: a thread has four states of a channel, so a state moves as 16 bytes, and takes four
+// sequences at a time: its decay rates serve all of them, its lanes of a channel share out the four softplus and
+// the four sums, and 64 bytes of state are under way.  Bound by the states' traffic.  init and final may be one
+// buffer: a thread reads its states before it writes them.
 template <typename T, int NP>
-__global__ void __launch_bounds__(256) k_ssm_step(Ssm s) {
-  constexpr int NL = NP / 4;
+__global__ void __launch_bounds__(256, 3) k_ssm_step(Ssm s) {
+  constexpr int NL = NP / 4, Q = 4, OWN = NL < Q ? Q / NL : 1;  // sequences whose softplus and sum a lane has
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = at / NL;
-  const int nl = (int)(at % NL), n0 = nl * 4;
-  const int64_t n = row / s.D, ch = row - n * s.D;
-  const bool live = n < s.seqs.n;
-  float a = 0.f;
-  if (live) {
-    const int64_t g = ch / (s.D / s.G);
-    const float* st = s.init + row * s.N;
-    float* nx = s.final + row * s.N;
-    const T* Bm = static_cast<const T*>(s.Bm) + n * s.ld_b + g * s.N;
-    const T* Cm = static_cast<const T*>(s.Cm) + n * s.ld_c + g * s.N;
-    float h[4], A2[4];
-    if (s.vec) {
-      const float4 v = *reinterpret_cast<const float4*>(st + n0);
-      h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
-    } else {
-      load_states(st, s.N, n0, h);
-    }
-    load_decay(s, ch, true, n0, A2);
-    const float x = up<T>(static_cast<const T*>(s.x)[n * s.ld_x + ch]);
-    float2 e;
-    const float v = up<T>(static_cast<const T*>(s.dt)[n * s.ld_dt + ch]) + (s.dt_bias ? s.dt_bias[ch] : 0.f);
-    const float d = softplus2({v, v}, e).x;
-    const float u = d * x;
-    a = nl == 0 && s.skip ? s.skip[ch] * x : 0.f;
+  const int64_t ch = at / NL;
+  const int lane = threadIdx.x & 31, nl = (int)(at % NL), n0 = nl * 4, first = lane & ~(NL - 1);
+  const bool live = ch < s.D;
+  const int slot = lane_slot<Q, NL>(nl);  // of lanes that share a sum, the first writes it
+  const int64_t g = live ? ch / (s.D / s.G) : 0, q0 = (int64_t)blockIdx.y * Q, step = (int64_t)gridDim.y * Q;
+  float A2[4];
+  load_decay(s, ch, live, n0, A2);
+  const float bias = live && s.dt_bias ? s.dt_bias[ch] : 0.f, skip = live && s.skip ? s.skip[ch] : 0.f;
+  const int64_t states = s.D * s.N;  // of a sequence
+  const float* st = s.init + q0 * states + ch * s.N + n0;
+  float* nx = s.final + q0 * states + ch * s.N + n0;
+  const T* Bm = static_cast<const T*>(s.Bm) + q0 * s.ld_b + g * s.N + n0;
+  const T* Cm = static_cast<const T*>(s.Cm) + q0 * s.ld_c + g * s.N + n0;
+  const T* x = static_cast<const T*>(s.x) + (q0 + slot) * s.ld_x + ch;
+  const T* dt = static_cast<const T*>(s.dt) + (q0 + slot) * s.ld_dt + ch;
+  T* y = static_cast<T*>(s.y) + (q0 + slot) * s.D + ch;
+  const bool some = live && n0 < s.N;
+  for (int64_t left = s.seqs.n - q0; left > 0; left -= step) {
+    float h[Q][4], xv[OWN], u[OWN], d[OWN], o[Q];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool in = n0 + j < s.N;
-      h[j] = fmaf(ex2(d * A2[j]), h[j], in ? u * up<T>(Bm[n0 + j]) : 0.f);
-      a = fmaf(h[j], in ? up<T>(Cm[n0 + j]) : 0.f, a);
+    for (int k = 0; k < Q; ++k) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[k][j] = 0.f;
+      if (some && k < left) {
+        if (s.vec)
+          load_padded(st + k * states, h[k]);
+        else
+          load_states(st + k * states, s.N - n0, 0, h[k]);
+      }
     }
-    if (s.vec)
-      *reinterpret_cast<float4*>(nx + n0) = make_float4(h[0], h[1], h[2], h[3]);
-    else
-      store_states(nx, s.N, n0, h);
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+      const bool in = live && slot + i < left;
+      xv[i] = in ? up<T>(x[i * s.ld_x]) : 0.f;
+      const float v = in ? up<T>(dt[i * s.ld_dt]) + bias : 0.f;
+      float2 e;
+      d[i] = softplus2({v, v}, e).x;
+      u[i] = d[i] * xv[i];
+    }
+#pragma unroll
+    for (int k = 0; k < Q; ++k) {
+      // the lane whose slot covers k, and the place there
+      constexpr int HAVE = NL < Q ? NL : Q;
+      int owner = 0;
+#pragma unroll
+      for (int l = 0; l < HAVE; ++l)
+        if (lane_slot<Q, NL>(l) == k / OWN * OWN) owner = l;
+      const float dk = __shfl_sync(0xffffffffu, d[k % OWN], first + owner), uk = __shfl_sync(0xffffffffu, u[k % OWN], first + owner);
+      float a = 0.f;
+      if (some && k < left) {
+        float b[4], c[4];
+        if (s.vec_bc) {
+          Pack<T, 4> pb, pc;
+          pb.load(Bm + k * s.ld_b), pc.load(Cm + k * s.ld_c);
+          pb.get(b), pc.get(c);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            b[j] = n0 + j < s.N ? up<T>(Bm[k * s.ld_b + j]) : 0.f;
+            c[j] = n0 + j < s.N ? up<T>(Cm[k * s.ld_c + j]) : 0.f;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          h[k][j] = fmaf(ex2(dk * A2[j]), h[k][j], uk * b[j]);
+          a = fmaf(h[k][j], c[j], a);
+        }
+        if (s.vec)
+          store_padded(nx + k * states, h[k]);
+        else
+          store_states(nx + k * states, s.N - n0, 0, h[k]);
+      }
+      o[k] = a;
+    }
+    lane_sums<Q, NL, 1>(o, lane);
+#pragma unroll
+    for (int i = 0; i < OWN; ++i)
+      if (live && slot + i < left && nl < Q) y[i * s.D] = down<T>(fmaf(skip, xv[i], o[i]));
+    st += step * states, nx += step * states, Bm += step * s.ld_b, Cm += step * s.ld_c;
+    x += step * s.ld_x, dt += step * s.ld_dt, y += step * s.D;
   }
-#pragma unroll
-  for (int o = NL / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-  if (live && nl == 0) static_cast<T*>(s.y)[row] = down<T>(a);
 }
 
 template <typename T, int NP>
@@ -283,9 +327,11 @@ cudaError_t forward(const Ssm& c, cudaStream_t s) {
 
 template <typename T, int NP>
 cudaError_t step(const Ssm& c, cudaStream_t s) {
-  const int64_t n = c.seqs.n * c.D * (NP / 4);
+  const int64_t across = (c.D * (NP / 4) + 255) / 256, groups = (c.seqs.n + 3) / 4;
+  // as many blocks as 16 for each of 148 multiprocessors; beyond that a block goes on to further sequences
+  const int64_t y = std::min<int64_t>(std::min<int64_t>(groups, 65535), std::max<int64_t>(1, 148 * 16 / across));
   ProfScope ps("ssm_step", s);
-  k_ssm_step<T, NP><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(c);
+  k_ssm_step<T, NP><<<dim3((unsigned)across, (unsigned)y), 256, 0, s>>>(c);
   return cudaGetLastError();
 }
 

@@ -23,14 +23,16 @@ def _p(t):
 
 
 def _call(fn, dev, *args):
-    """The entry point on the current stream of `dev`."""
+    """The entry point on the current stream of `dev` (its raw handle: building a Stream object costs more than a
+    small kernel takes)."""
     if dev.type != "cuda":
         raise ValueError(f"{fn}: expected CUDA tensors, got {dev}")
-    if dev.index == torch.cuda.current_device():
-        rc = getattr(lib, fn)(*args, torch.cuda.current_stream().cuda_stream)
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    if dev.index == torch._C._cuda_getDevice():
+        rc = getattr(lib, fn)(*args, stream)
     else:
         with torch.cuda.device(dev):
-            rc = getattr(lib, fn)(*args, torch.cuda.current_stream().cuda_stream)
+            rc = getattr(lib, fn)(*args, stream)
     if rc != GDN_OK:
         raise GDNError(fn, rc)
 
