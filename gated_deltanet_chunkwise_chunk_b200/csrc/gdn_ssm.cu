@@ -156,10 +156,10 @@ __global__ void __launch_bounds__(Shape<NP, kFwd>::NT, 3) k_ssm_fwd(Ssm s) {
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float2 e = __fmul2_rn(d2[k], {A2[j], A2[j]}), u = __fmul2_rn(u2[k], b2[k]);
+            const float2 a = decays<T>(__fmul2_rn(d2[k], {A2[j], A2[j]})), u = __fmul2_rn(u2[k], b2[k]);
             float2 hh;
-            hh.x = fmaf(ex2(e.x), h[j], u.x);
-            hh.y = fmaf(ex2(e.y), hh.x, u.y);
+            hh.x = fmaf(a.x, h[j], u.x);
+            hh.y = fmaf(a.y, hh.x, u.y);
             h[j] = hh.y;
             if (!END) y2[k] = __ffma2_rn(hh, c2[k], y2[k]);
           }
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(256) k_ssm_join(Ssm s) {
     float* p = s.starts + state_at<NP>(s, u0 + k, ch, n);
     const float end = *p;
     *p = h;
-    if (k + 1 < segs) h = fmaf(ex2(A2 * s.sums[(u0 + k) * s.D + ch]), h, end);
+    if (k + 1 < segs) h = fmaf(ex2_exact({A2 * s.sums[(u0 + k) * s.D + ch], 0.f}).x, h, end);
   }
 }
 
@@ -283,9 +283,12 @@ __global__ void __launch_bounds__(256, 3) k_ssm_step(Ssm s) {
           }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          h[k][j] = fmaf(ex2(dk * A2[j]), h[k][j], uk * b[j]);
+        for (int j = 0; j < 4; j += 2) {
+          const float2 e = decays<T>({dk * A2[j], dk * A2[j + 1]});
+          h[k][j] = fmaf(e.x, h[k][j], uk * b[j]);
+          h[k][j + 1] = fmaf(e.y, h[k][j + 1], uk * b[j + 1]);
           a = fmaf(h[k][j], c[j], a);
+          a = fmaf(h[k][j + 1], c[j + 1], a);
         }
         if (s.vec)
           store_padded(nx + k * states, h[k]);

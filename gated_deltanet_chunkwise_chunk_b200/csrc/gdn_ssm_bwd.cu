@@ -213,9 +213,9 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
             const float2 c2[2] = {{cv.x, cv.y}, {cv.z, cv.w}};
 #pragma unroll
             for (int k = 1; k >= 0; --k) {
-              const float2 e = __fmul2_rn(d2[k], {A2[j], A2[j]});
-              ga[j] = ex2(e.y) * fmaf(c2[k].y, g2[k].y, ga[j]);
-              ga[j] = ex2(e.x) * fmaf(c2[k].x, g2[k].x, ga[j]);
+              const float2 e = decays<T>(__fmul2_rn(d2[k], {A2[j], A2[j]}));
+              ga[j] = e.y * fmaf(c2[k].y, g2[k].y, ga[j]);
+              ga[j] = e.x * fmaf(c2[k].x, g2[k].x, ga[j]);
             }
           }
         }
@@ -239,9 +239,9 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int t = 4 * q + 2 * k;
-              const float2 e = __fmul2_rn(d2[k], {A2[j], A2[j]}), u = __fmul2_rn(__fmul2_rn(d2[k], x2[k]), b2[k]);
-              a[t][j] = ex2(e.x);
-              a[t + 1][j] = ex2(e.y);
+              const float2 e = decays<T>(__fmul2_rn(d2[k], {A2[j], A2[j]})), u = __fmul2_rn(__fmul2_rn(d2[k], x2[k]), b2[k]);
+              a[t][j] = e.x;
+              a[t + 1][j] = e.y;
               h[t][j] = fmaf(a[t][j], t > 0 ? h[t > 0 ? t - 1 : 0][j] : h0[j], u.x);
               h[t + 1][j] = fmaf(a[t + 1][j], h[t][j], u.y);
             }
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(256) k_ssm_bwd_join(Ssm s) {
     float* p = s.starts + state_at<NP>(s, u0 + k, ch, n);
     const float front = *p;
     *p = g;
-    if (k > 0) g = fmaf(ex2(A2 * s.sums[(u0 + k) * s.D + ch]), g, front);
+    if (k > 0) g = fmaf(ex2_exact({A2 * s.sums[(u0 + k) * s.D + ch], 0.f}).x, g, front);
   }
 }
 
