@@ -165,7 +165,7 @@ template <typename T, int V, int W>
 __global__ void __launch_bounds__(NT, W <= 4 ? 2 : 1) k_conv_fwd(Conv c, int lg, int strip) {
   extern __shared__ __align__(16) char shared[];
   if (bad_call(c.seqs)) return;
-  Piece p;
+  Piece p{};
   if (!find_piece(c.seqs, blockIdx.x, lg, p)) return;
   const int cols = blockDim.x * V;
   const int64_t c0 = (int64_t)blockIdx.y * cols, ch = c0 + threadIdx.x * V;
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(NT, W <= 4 ? 2 : 1) k_conv_bwd(Conv c, int lg)
   __shared__ float red[NT * V];
   constexpr int N = Pairs<V>::N, GR = kHalf / W * W, STEPS = BS + W - 1;
   if (bad_call(c.seqs)) return;
-  Piece p;
+  Piece p{};
   const bool some = find_piece(c.seqs, blockIdx.x, lg, p);
   const int cols = blockDim.x * V;
   const int64_t c0 = (int64_t)blockIdx.y * cols, ch = c0 + threadIdx.x * V;

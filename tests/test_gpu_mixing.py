@@ -213,6 +213,14 @@ def test_scan_of_long_sequences(lengths, packed, D, N):
     _scan_check(*_scan_case(3, lengths, packed, D, N, 1, F32), lengths)
 
 
+@pytest.mark.parametrize("lengths,packed,D,N,G", [([900], False, 8, 16, 1), ([2000, 3, 0, 1100], True, 16, 16, 2), ([1025, 1025], False, 4, 5, 1),
+                                                  ([800], True, 3, 33, 1)])
+def test_scan_cut_in_both_directions(lengths, packed, D, N, G):
+    """Long enough that the forward is cut along time too, with tails of odd lengths and an empty sequence between."""
+    for dtype in (F32, BF):
+        _scan_check(*_scan_case(5, lengths, packed, D, N, G, dtype), lengths)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF, FP])
 @pytest.mark.parametrize("B,D,N,G,in_place", [(1, 8, 16, 1, True), (3, 33, 16, 1, False), (9, 24, 5, 2, True), (2, 40, 64, 1, True), (70, 16, 32, 4, False)])
 def test_scan_step(B, D, N, G, in_place, dtype):
@@ -250,6 +258,46 @@ def test_scan_extremes():
     c["dt"][0, 48] = 1.0
     y, fin = _gdn().ssm_scan_fwd(**c, initial_state=init)
     assert torch.isfinite(y).all() and torch.isfinite(fin).all()
+
+
+def _short_memory(T, D, dtype):
+    """Inputs whose states forget within a few tokens (delta A <= -3 for every state), so that a call's last tokens
+    can be computed from the few before them."""
+    gen = torch.Generator().manual_seed(T)
+    x = torch.empty(1, T, D, dtype=dtype, device="cuda").uniform_(-1, 1)
+    dt = torch.full((1, T, D), 3.0, dtype=dtype, device="cuda")
+    Bm, Cm = (torch.empty(1, T, 1, 4, dtype=dtype, device="cuda").uniform_(-1, 1) for _ in range(2))
+    return x, dt, torch.zeros(D, 4, device="cuda"), Bm, Cm, _rand(gen, D)
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: the ends of a call's tensors agree with a short call on them."""
+    gdn = _gdn()
+    D, T = 2048, (1 << 20) + 40
+    x, dt, A_log, Bm, Cm, skip = _short_memory(T, D, BF)
+    y, st = gdn.ssm_scan_fwd(x, dt, A_log, Bm, Cm, skip)
+    tail = [t[:, -64:].contiguous() for t in (x, dt, Bm, Cm)]
+    y2, st2 = gdn.ssm_scan_fwd(tail[0], tail[1], A_log, tail[2], tail[3], skip)
+    # 32 tokens back a state is e^-96 of itself, far below half a step of its fp32 value
+    assert torch.equal(y[:, -32:], y2[:, -32:]) and torch.equal(st, st2)
+    del dt, y, Bm, Cm
+    gen = torch.Generator().manual_seed(1)
+    w, b = _rand(gen, D, 4), _rand(gen, D)
+    y, fin = gdn.causal_conv_fwd(x, w, b, output_final_state=True)
+    y2, fin2 = gdn.causal_conv_fwd(tail[0], w, b, output_final_state=True)
+    assert torch.equal(y[:, -60:], y2[:, -60:]) and torch.equal(fin, fin2)
+    g = gdn.causal_conv_bwd(x, w, y, b)
+    g2 = gdn.causal_conv_bwd(tail[0], w, y[:, -64:].contiguous(), b)
+    assert torch.equal(g["dx"][:, -60:], g2["dx"][:, -60:])
+    del g
+    n, stats = gdn.layer_norm_fwd(x, w[:, 0].contiguous(), rms=True)
+    n2, stats2 = gdn.layer_norm_fwd(tail[0], w[:, 0].contiguous(), rms=True)
+    # (a different split of a row over threads: the same to the rounding of its sums)
+    half = torch.finfo(BF).eps
+    assert (n[:, -64:].float() - n2.float()).abs().max() <= half * n2.float().abs().max()
+    g = gdn.layer_norm_bwd(x, y, stats, w[:, 0].contiguous(), rms=True)
+    g2 = gdn.layer_norm_bwd(tail[0], y[:, -64:].contiguous(), stats2, w[:, 0].contiguous(), rms=True)
+    assert (g["dx"][:, -64:].float() - g2["dx"].float()).abs().max() <= half * g2["dx"].float().abs().max()
 
 
 # ---------------------------------------------------------------------------------- norm
