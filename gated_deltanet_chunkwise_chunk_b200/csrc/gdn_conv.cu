@@ -5,7 +5,13 @@
 //   dx[t] = sum_j w[d, j] dpre[t + (W-1) - j],  dw[d, j] = sum_t dpre[t] x[t - (W-1) + j],
 //   dbias = sum_t dpre[t].
 // All three directions move bytes: the taps are kept in registers and every input row is read from
-// HBM once (neighbouring strips of tokens meet in L1 and L2).
+// HBM once (neighbouring strips of tokens meet in L1 and L2).  What it takes to move them at speed: rows on
+// their way ahead of their use (asynchronous copies into rings of the thread's own), taps read in memory
+// order through shared memory (32 strided loads a thread cost more than the rows: 204 us instead of 68
+// forward), and packed multiply-adds.  Measured at 2 x 8192 x 4096 bf16 with four taps and the silu: forward
+// 68 us for 268 MB (4.0 TB/s), bound by latency at two blocks a multiprocessor and by the exponentials and
+// reciprocals (half their pipe); backward 139 us for 403 MB (2.9 TB/s), bound by issue (36 instructions an
+// element); 256 single tokens of 4096 channels 10 us.
 #include <algorithm>
 
 #include "mix_common.cuh"

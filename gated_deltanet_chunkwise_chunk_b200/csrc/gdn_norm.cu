@@ -7,8 +7,12 @@
 // once and y (dx, dz) written once.  A row belongs to a group of 1 to 32 lanes (up to 512 elements,
 // several rows to a block) or to a block of up to 512 threads; each thread holds NV vectors of it.  The variance
 // is the mean of (x - mu)^2 over the registers, not a difference of sums.  The backward's blocks walk
-// over many rows with the weight's and bias's sums in registers and the next row's loads in flight;
+// over many rows with the weight's and bias's sums in registers and the next rows' loads in flight;
 // their partial rows are added in block order by a second kernel, so the sums do not depend on timing.
+// Measured (bf16): rows of 4096, 8192 of them, with weight and bias: forward 36 us for 134 MB (3.7 TB/s), backward
+// 59 us for 201 MB (3.4 TB/s); gated rms rows of 128, 262144 of them: forward 47 us for 201 MB (4.3 TB/s), backward
+// 95 us for 335 MB (3.5 TB/s).  What remains is issue and latency: a row's sums cost its threads as much as eight
+// elements, so a thread has 16 to 32 of them, which leaves eight to sixteen warps a multiprocessor.
 #include <algorithm>
 
 #include "mix_common.cuh"

@@ -21,6 +21,12 @@ struct FwdShared {
   alignas(16) T rc[kRing<T, NP>][END ? 8 : kTile * NP];
 };
 
+// Measured (bf16, N = 16): 1 x 32768 x 4096 1.39 ms, with one block on each of 128 multiprocessors, bound by the
+// latency of its four working warps (issue 42%, shared memory 56%, exponentials 40% of their peaks); 8 x 1024 x 4096
+// 246 us, where shared memory binds (87%: a 16-byte load is four wavefronts however many lanes want the same
+// words, 10 bytes a state and token).  The bytes alone would take 123 and 31 us, the exponentials 0.55 ms and 0.14.
+// Tried and slower: two states a lane (1.58 ms), the sums over lanes left to the feeding warps (1.54 ms), two
+// channels a lane (within 15% either way).
 // One segment.  END: only the state at its end from a zero state, and the sum of its deltas (the first
 // pass over segments that have one behind them).
 // 16 tokens at a time: their exponentials do not wait for the states, and their 16 sums over the states are
@@ -212,22 +218,26 @@ __global__ void __launch_bounds__(256) k_ssm_join(Ssm s) {
   }
 }
 
-// One token for each sequence: a thread has four states of a channel, so a state moves as 16 bytes, and takes four
-// sequences at a time: its decay rates serve all of them, its lanes of a channel share out the four softplus and
-// the four sums, and 64 bytes of state are under way.  Bound by the states' traffic.  init and final may be one
-// buffer: a thread reads its states before it writes them.
-template <typename T, int NP>
+// One token for each sequence: a thread has four states of a channel, so a state moves as 16 bytes, and goes through
+// the sequences four at a time: its decay rates serve all of them, and its lanes of a channel share out the four
+// softplus and the four sums.  Bound by the states' traffic.  RING: the states, B and C of the next two groups of
+// four are on their way through shared memory of the thread's own (asynchronous 16- and 8-byte copies).  Without:
+// plain loads, for calls of few sequences, which gain nothing from a ring (one request x 4096 x 16: 7.6 us, with the
+// ring 9.7), and where N or the alignment of B and C does not allow the copies.  256 requests x 4096 x 16: 35 us for
+// the 141 MB that they read and write (4.0 TB/s), without the ring 46.  init and final may be one buffer: a thread
+// reads its states before it writes them, and no other touches them.
+template <typename T, int NP, bool RING>
 __global__ void __launch_bounds__(256, 3) k_ssm_step(Ssm s) {
   constexpr int NL = NP / 4, Q = 4, OWN = NL < Q ? Q / NL : 1;  // sequences whose softplus and sum a lane has
+  constexpr int MAT = 4 * (int)sizeof(T);                       // bytes of four values of B or C
+  extern __shared__ __align__(16) char shared[];                // [2][Q][256] states, then B, then C
+  const unsigned ring = (unsigned)__cvta_generic_to_shared(shared);
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t ch = at / NL;
   const int lane = threadIdx.x & 31, nl = (int)(at % NL), n0 = nl * 4, first = lane & ~(NL - 1);
   const bool live = ch < s.D;
   const int slot = lane_slot<Q, NL>(nl);  // of lanes that share a sum, the first writes it
   const int64_t g = live ? ch / (s.D / s.G) : 0, q0 = (int64_t)blockIdx.y * Q, step = (int64_t)gridDim.y * Q;
-  float A2[4];
-  load_decay(s, ch, live, n0, A2);
-  const float bias = live && s.dt_bias ? s.dt_bias[ch] : 0.f, skip = live && s.skip ? s.skip[ch] : 0.f;
   const int64_t states = s.D * s.N;  // of a sequence
   const float* st = s.init + q0 * states + ch * s.N + n0;
   float* nx = s.final + q0 * states + ch * s.N + n0;
@@ -237,28 +247,63 @@ __global__ void __launch_bounds__(256, 3) k_ssm_step(Ssm s) {
   const T* dt = static_cast<const T*>(s.dt) + (q0 + slot) * s.ld_dt + ch;
   T* y = static_cast<T*>(s.y) + (q0 + slot) * s.D + ch;
   const bool some = live && n0 < s.N;
-  for (int64_t left = s.seqs.n - q0; left > 0; left -= step) {
+  int64_t left = s.seqs.n - q0, to_ask = left;
+  auto at_state = [&](int half, int k) { return ring + ((half * Q + k) * 256 + threadIdx.x) * 16; };
+  auto at_mat = [&](int half, int k, int which) { return ring + 2 * Q * 256 * 16 + (((which * 2 + half) * Q + k) * 256 + threadIdx.x) * MAT; };
+  auto ask = [&](int half) {
+    if constexpr (RING) {
+#pragma unroll
+      for (int k = 0; k < Q; ++k) {
+        const bool in = some && k < to_ask;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at_state(half, k)), "l"(in ? st + k * states : s.init), "r"(in ? 16 : 0) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at_mat(half, k, 0)), "l"(in ? static_cast<const void*>(Bm + k * s.ld_b) : s.Bm), "n"(MAT), "r"(in ? MAT : 0) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at_mat(half, k, 1)), "l"(in ? static_cast<const void*>(Cm + k * s.ld_c) : s.Cm), "n"(MAT), "r"(in ? MAT : 0) : "memory");
+      }
+      copy_commit();
+      st += step * states, Bm += step * s.ld_b, Cm += step * s.ld_c;
+      to_ask -= step;
+    }
+  };
+  T xr[OWN], tr[OWN];
+  auto fetch = [&](int64_t have) {
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+      xr[i] = tr[i] = down<T>(0.f);
+      if (live && slot + i < have) xr[i] = x[i * s.ld_x], tr[i] = dt[i * s.ld_dt];
+    }
+  };
+  ask(0);
+  ask(1);
+  fetch(left);
+  float A2[4];
+  load_decay(s, ch, live, n0, A2);
+  const float bias = live && s.dt_bias ? s.dt_bias[ch] : 0.f, skip = live && s.skip ? s.skip[ch] : 0.f;
+  for (int half = 0; left > 0; left -= step, half ^= 1) {
     float h[Q][4], xv[OWN], u[OWN], d[OWN], o[Q];
+    if constexpr (!RING) {
 #pragma unroll
-    for (int k = 0; k < Q; ++k) {
+      for (int k = 0; k < Q; ++k) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[k][j] = 0.f;
-      if (some && k < left) {
-        if (s.vec)
-          load_padded(st + k * states, h[k]);
-        else
-          load_states(st + k * states, s.N - n0, 0, h[k]);
+        for (int j = 0; j < 4; ++j) h[k][j] = 0.f;
+        if (some && k < left) {
+          if (s.vec)
+            load_padded(st + k * states, h[k]);
+          else
+            load_states(st + k * states, s.N - n0, 0, h[k]);
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < OWN; ++i) {
-      const bool in = live && slot + i < left;
-      xv[i] = in ? up<T>(x[i * s.ld_x]) : 0.f;
-      const float v = in ? up<T>(dt[i * s.ld_dt]) + bias : 0.f;
+      xv[i] = up<T>(xr[i]);
+      const float v = up<T>(tr[i]) + bias;
       float2 e;
       d[i] = softplus2({v, v}, e).x;
       u[i] = d[i] * xv[i];
     }
+    x += step * s.ld_x, dt += step * s.ld_dt;
+    fetch(left - step);
+    if constexpr (RING) copy_wait<1>();
 #pragma unroll
     for (int k = 0; k < Q; ++k) {
       // the lane whose slot covers k, and the place there
@@ -271,9 +316,16 @@ __global__ void __launch_bounds__(256, 3) k_ssm_step(Ssm s) {
       float a = 0.f;
       if (some && k < left) {
         float b[4], c[4];
-        if (s.vec_bc) {
+        if constexpr (RING) {
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(h[k][0]), "=f"(h[k][1]), "=f"(h[k][2]), "=f"(h[k][3]) : "r"(at_state(half, k)) : "memory");
           Pack<T, 4> pb, pc;
-          pb.load(Bm + k * s.ld_b), pc.load(Cm + k * s.ld_c);
+          if constexpr (MAT == 8) {
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(pb.u[0]), "=r"(pb.u[1]) : "r"(at_mat(half, k, 0)) : "memory");
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(pc.u[0]), "=r"(pc.u[1]) : "r"(at_mat(half, k, 1)) : "memory");
+          } else {
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(pb.u[0]), "=r"(pb.u[1]), "=r"(pb.u[2]), "=r"(pb.u[3]) : "r"(at_mat(half, k, 0)) : "memory");
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(pc.u[0]), "=r"(pc.u[1]), "=r"(pc.u[2]), "=r"(pc.u[3]) : "r"(at_mat(half, k, 1)) : "memory");
+          }
           pb.get(b), pc.get(c);
         } else {
 #pragma unroll
@@ -290,20 +342,22 @@ __global__ void __launch_bounds__(256, 3) k_ssm_step(Ssm s) {
           a = fmaf(h[k][j], c[j], a);
           a = fmaf(h[k][j + 1], c[j + 1], a);
         }
-        if (s.vec)
+        if (RING || s.vec)
           store_padded(nx + k * states, h[k]);
         else
           store_states(nx + k * states, s.N - n0, 0, h[k]);
       }
       o[k] = a;
     }
+    ask(half);
     lane_sums<Q, NL, 1>(o, lane);
 #pragma unroll
     for (int i = 0; i < OWN; ++i)
       if (live && slot + i < left && nl < Q) y[i * s.D] = down<T>(fmaf(skip, xv[i], o[i]));
-    st += step * states, nx += step * states, Bm += step * s.ld_b, Cm += step * s.ld_c;
-    x += step * s.ld_x, dt += step * s.ld_dt, y += step * s.D;
+    nx += step * states, y += step * s.D;
+    if constexpr (!RING) st += step * states, Bm += step * s.ld_b, Cm += step * s.ld_c;
   }
+  copy_wait<0>();
 }
 
 template <typename T, int NP>
@@ -331,10 +385,17 @@ cudaError_t forward(const Ssm& c, cudaStream_t s) {
 template <typename T, int NP>
 cudaError_t step(const Ssm& c, cudaStream_t s) {
   const int64_t across = (c.D * (NP / 4) + 255) / 256, groups = (c.seqs.n + 3) / 4;
-  // as many blocks as 16 for each of 148 multiprocessors; beyond that a block goes on to further sequences
-  const int64_t y = std::min<int64_t>(std::min<int64_t>(groups, 65535), std::max<int64_t>(1, 148 * 16 / across));
+  // with the ring, three blocks for each of 148 multiprocessors; without, as many as there are, up to 16
+  const int64_t most = std::min<int64_t>(groups, 65535), ring = std::max<int64_t>(1, 148 * 3 / across);
   ProfScope ps("ssm_step", s);
-  k_ssm_step<T, NP><<<dim3((unsigned)across, (unsigned)y), 256, 0, s>>>(c);
+  if (c.vec && c.vec_bc && groups >= 4 * ring) {
+    constexpr size_t bytes = 2 * 4 * 256 * (16 + 8 * sizeof(T));
+    if (cudaError_t e = allow_shared(k_ssm_step<T, NP, true>, bytes)) return e;
+    k_ssm_step<T, NP, true><<<dim3((unsigned)across, (unsigned)ring), 256, bytes, s>>>(c);
+  } else {
+    const dim3 grid((unsigned)across, (unsigned)std::min(most, std::max<int64_t>(1, 148 * 16 / across)));
+    k_ssm_step<T, NP, false><<<grid, 256, 0, s>>>(c);
+  }
   return cudaGetLastError();
 }
 

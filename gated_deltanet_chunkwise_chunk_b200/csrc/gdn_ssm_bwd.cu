@@ -11,6 +11,10 @@
 // and what it hands over are always the same registers and a butterfly step is a shuffle and an addition.
 // The feeding warps add the block's warps in shared memory, and the blocks of a group's channels leave
 // partial rows that a second kernel adds in order.  Nothing is atomic.
+// Measured at 2 x 4096 x 2048 x 16 bf16: 404 us in four segments a sequence (82 us for the first pass over them,
+// 20 for the second kernel); 569 us uncut.  Bound by shared memory (65%) and instruction issue (44%, 92 for a
+// token and scheduler) with eight working warps a multiprocessor: the sums over a warp's channels are a third of
+// the instructions.  With 184 and 176 registers instead of 192 for the working warps 407 and 457 us.
 #include <algorithm>
 #include <type_traits>
 

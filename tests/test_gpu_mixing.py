@@ -222,7 +222,8 @@ def test_scan_cut_in_both_directions(lengths, packed, D, N, G):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF, FP])
-@pytest.mark.parametrize("B,D,N,G,in_place", [(1, 8, 16, 1, True), (3, 33, 16, 1, False), (9, 24, 5, 2, True), (2, 40, 64, 1, True), (70, 16, 32, 4, False)])
+@pytest.mark.parametrize("B,D,N,G,in_place", [(1, 8, 16, 1, True), (3, 33, 16, 1, False), (9, 24, 5, 2, True), (2, 40, 64, 1, True), (70, 16, 32, 4, False),
+                                             (301, 2048, 16, 1, True), (130, 4096, 8, 2, False), (90, 4100, 12, 1, True)])
 def test_scan_step(B, D, N, G, in_place, dtype):
     gdn = _gdn()
     c, st, _, _ = _scan_case(B + N, [1] * B, False, D, N, G, dtype)
