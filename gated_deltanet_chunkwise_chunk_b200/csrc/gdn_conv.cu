@@ -121,8 +121,8 @@ __device__ __forceinline__ float2 sigmoid2(float2 a) {
 }
 
 // A thread's own rows on their way through shared memory: two halves of kHalf rows, one under way while the other
-// is worked on.  Nobody else touches them, so they need no barrier.  Narrow elements without an asynchronous copy
-// of their size are loaded as they are asked for.
+// is worked on.  Nobody else touches them, so they need no barrier.  Single half words, which have no asynchronous
+// copy, go through registers.
 constexpr int kHalf = 8;
 
 template <typename T, int V>
@@ -141,11 +141,10 @@ struct Ring {
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + k * SLOT), "l"(src), "r"(in ? 16 : 0) : "memory");
     } else if constexpr (BYTES >= 4) {
       asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to + k * SLOT), "l"(src), "n"(BYTES), "r"(in ? BYTES : 0) : "memory");
-    } else {
-      const unsigned v = in ? *reinterpret_cast<const unsigned short*>(src) : 0u;
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + k * SLOT), "r"(v) : "memory");
     }
   }
+  // the k-th row of a half word, loaded by the caller (all of a half's before the first is put)
+  __device__ __forceinline__ void put(int k, unsigned v) const { asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + k * SLOT), "r"(v) : "memory"); }
   __device__ __forceinline__ Pack<T, V> get(int k) const {
     Pack<T, V> r;
     const unsigned at = from + k * SLOT;
@@ -183,8 +182,16 @@ __global__ void __launch_bounds__(NT, W <= 4 ? 2 : 1) k_conv_fwd(Conv c, int lg,
   const T* x = static_cast<const T*>(c.x) + (p.t0 - p.pos + s0) * c.ld + ch;  // the next row to ask for
   int left = s1 - s0;
   auto ask = [&](int way) {
+    if constexpr (Ring<T, V>::BYTES >= 4) {
 #pragma unroll
-    for (int k = 0; k < GR; ++k, x += c.ld) ring.ask(k, x, k < left);
+      for (int k = 0; k < GR; ++k, x += c.ld) ring.ask(k, x, k < left);
+    } else {
+      unsigned v[GR];
+#pragma unroll
+      for (int k = 0; k < GR; ++k, x += c.ld) v[k] = k < left ? *reinterpret_cast<const unsigned short*>(x) : 0u;
+#pragma unroll
+      for (int k = 0; k < GR; ++k) ring.put(k, v[k]);
+    }
     left -= GR;
     ring.commit();
     ring.filled(way);
@@ -267,10 +274,21 @@ __global__ void __launch_bounds__(NT, W <= 4 ? 2 : 1) k_conv_bwd(Conv c, int lg)
   const T* dy = static_cast<const T*>(c.dy) + (bos + s0) * c.D + ch;
   int left = busy ? min(STEPS, p.slen - s0) : 0;
   auto ask = [&](int way) {
+    if constexpr (Ring<T, V>::BYTES >= 4) {
 #pragma unroll
-    for (int k = 0; k < GR; ++k, x += c.ld, dy += c.D) {
-      xs.ask(k, x, k < left);
-      gs.ask(k, dy, k < left);
+      for (int k = 0; k < GR; ++k, x += c.ld, dy += c.D) {
+        xs.ask(k, x, k < left);
+        gs.ask(k, dy, k < left);
+      }
+    } else {
+      unsigned v[GR], g[GR];
+#pragma unroll
+      for (int k = 0; k < GR; ++k, x += c.ld, dy += c.D) {
+        v[k] = k < left ? *reinterpret_cast<const unsigned short*>(x) : 0u;
+        g[k] = k < left ? *reinterpret_cast<const unsigned short*>(dy) : 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < GR; ++k) xs.put(k, v[k]), gs.put(k, g[k]);
     }
     left -= GR;
     xs.commit();
@@ -453,7 +471,8 @@ int log2i(int x) {
   return l;
 }
 
-// Whole 16-byte (backward: four-element) vectors need widths, strides and bases that are multiples.
+// Vectors of V elements need widths, strides and bases that are multiples: 16 bytes forward, four elements backward,
+// or else the 4-byte words of an even width.
 bool vec_ok(const Conv& c, int es, int V) {
   const uintptr_t b = (uintptr_t)es * V;
   if (c.D % V || c.ld % V) return false;
@@ -528,10 +547,12 @@ template <int WHAT>
 cudaError_t dispatch(const Conv& c, cudaStream_t s) {
   if (c.dtype == GDN_DTYPE_FP32)
     return vec_ok(c, 4, 4) ? by_width<WHAT, float, 4>(c, s) : by_width<WHAT, float, 1>(c, s);
-  const bool v = vec_ok(c, 2, WHAT == BWD ? 4 : 8);
+  const int V = vec_ok(c, 2, WHAT == BWD ? 4 : 8) ? 8 : vec_ok(c, 2, 2) ? 2 : 1;
   if (c.dtype == GDN_DTYPE_BF16)
-    return v ? by_width<WHAT, __nv_bfloat16, 8>(c, s) : by_width<WHAT, __nv_bfloat16, 1>(c, s);
-  return v ? by_width<WHAT, __half, 8>(c, s) : by_width<WHAT, __half, 1>(c, s);
+    return V == 8   ? by_width<WHAT, __nv_bfloat16, 8>(c, s)
+           : V == 2 ? by_width<WHAT, __nv_bfloat16, 2>(c, s)
+                    : by_width<WHAT, __nv_bfloat16, 1>(c, s);
+  return V == 8 ? by_width<WHAT, __half, 8>(c, s) : V == 2 ? by_width<WHAT, __half, 2>(c, s) : by_width<WHAT, __half, 1>(c, s);
 }
 
 }  // namespace

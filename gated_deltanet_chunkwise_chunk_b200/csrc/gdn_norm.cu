@@ -64,14 +64,16 @@ __device__ __forceinline__ int64_t row_at(int64_t r, int64_t inner, int64_t ld, 
 
 // A thread's own vectors of the rows to come, DEEP rows ahead, on their way through shared memory (nobody else
 // touches them, so they need no barrier).  ARR tensors of NV vectors, and a row's statistics.  DEEP: four, or as
-// many as leave room for a second block.
+// many as leave room for a second block.  Single half words, which have no asynchronous copy, wait one row ahead in
+// registers.
 template <typename T, int V, int NV, int ARR, int MOST>
 struct Ahead {
   static constexpr int BYTES = V * (int)sizeof(T), WIDTH = BYTES < 4 ? 4 : BYTES, ROW = ARR * NV * WIDTH + 8;
-  static constexpr int FIT = 104 * 1024 / (ROW * MOST), DEEP = FIT < 2 ? 2 : FIT > 4 ? 4 : FIT;
+  static constexpr int FIT = 104 * 1024 / (ROW * MOST), DEEP = BYTES < 4 ? 1 : FIT < 2 ? 2 : FIT > 4 ? 4 : FIT;
   static constexpr size_t bytes(int threads) { return (size_t)DEEP * ROW * threads; }
   unsigned base;
   int threads;
+  unsigned short held[BYTES < 4 ? ARR * NV : 1];
 
   __device__ __forceinline__ Ahead(const char* shared) : base((unsigned)__cvta_generic_to_shared(shared)), threads(blockDim.x) {}
   // thread-interleaved: vector v of a slot at [slot][v][thread], the statistics behind them
@@ -79,19 +81,25 @@ struct Ahead {
     return base + slot * ROW * threads + (v * threads + threadIdx.x) * WIDTH;
   }
   __device__ __forceinline__ unsigned stat_at(int slot) const { return base + (slot * ROW + ARR * NV * WIDTH) * threads + threadIdx.x * 8; }
-  __device__ __forceinline__ void ask(int slot, int v, const T* src, bool in) const {
+  __device__ __forceinline__ void ask(int slot, int v, const T* src, bool in) {
     if constexpr (BYTES == 16)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at(slot, v)), "l"(src), "r"(in ? 16 : 0) : "memory");
     else if constexpr (BYTES >= 4)
       asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at(slot, v)), "l"(src), "n"(BYTES), "r"(in ? BYTES : 0) : "memory");
-    else
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(at(slot, v)), "r"(in ? (unsigned)*reinterpret_cast<const unsigned short*>(src) : 0u) : "memory");
+    else {
+      held[v] = 0;
+      if (in) held[v] = *reinterpret_cast<const unsigned short*>(src);
+    }
   }
   __device__ __forceinline__ void ask_stats(int slot, const float* src, bool in) const {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(stat_at(slot)), "l"(src), "r"(in ? 8 : 0) : "memory");
   }
   __device__ __forceinline__ Pack<T, V> get(int slot, int v) const {
     Pack<T, V> r;
+    if constexpr (BYTES < 4) {
+      r.u[0] = held[v];
+      return r;
+    }
     const unsigned a = at(slot, v);
     if constexpr (BYTES == 16)
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.u[0]), "=r"(r.u[1]), "=r"(r.u[2]), "=r"(r.u[3]) : "r"(a) : "memory");
@@ -115,7 +123,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : NG) k_norm_fwd(Norm c, int lanes
   extern __shared__ __align__(16) char shared[];
   __shared__ float sh[2][2][32];
   using A = Ahead<T, V, NV, 2, BLOCK ? 512 : NG>;
-  const A ahead(shared);
+  A ahead(shared);
   const int lane = BLOCK ? threadIdx.x : threadIdx.x & (lanes - 1);
   const int rpb = BLOCK ? 1 : NG / lanes;
   const int64_t step = (int64_t)gridDim.x * rpb;
@@ -215,7 +223,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : NG) k_norm_bwd(Norm c, int lanes
   __shared__ float sh[2][2][32];
   __shared__ float red[BLOCK ? 1 : NG * V];
   using A = Ahead<T, V, NV, 3, BLOCK ? 512 : NG>;
-  const A ahead(shared);
+  A ahead(shared);
   const int lane = BLOCK ? threadIdx.x : threadIdx.x & (lanes - 1);
   const int rpb = BLOCK ? 1 : NG / lanes;
   const int64_t step = (int64_t)gridDim.x * rpb;
@@ -430,12 +438,12 @@ __global__ void __launch_bounds__(1024) k_norm_bwd_wide(Norm c) {
   }
 }
 
-bool vec_ok(const Norm& c, int es) {
-  const int V = 16 / es;
+// Vectors of V elements need widths, strides and bases that are multiples.
+bool vec_ok(const Norm& c, int es, int V) {
   if (c.D % V || c.ld_x % V || (c.gate && c.ld_z % V)) return false;
   const void* ps[] = {c.x, c.gate, c.y, c.dy, c.dx, c.dgate};
   for (const void* p : ps)
-    if (reinterpret_cast<uintptr_t>(p) % 16) return false;
+    if (reinterpret_cast<uintptr_t>(p) % ((uintptr_t)V * es)) return false;
   return true;
 }
 
@@ -523,11 +531,13 @@ cudaError_t launch(const Norm& c, cudaStream_t s, int64_t* blocks) {
 
 template <bool BWD>
 cudaError_t dispatch(const Norm& c, cudaStream_t s, int64_t* n) {
-  if (c.dtype == GDN_DTYPE_FP32) return vec_ok(c, 4) ? launch<float, 4, BWD>(c, s, n) : launch<float, 1, BWD>(c, s, n);
-  const bool v = vec_ok(c, 2);
+  if (c.dtype == GDN_DTYPE_FP32) return vec_ok(c, 4, 4) ? launch<float, 4, BWD>(c, s, n) : launch<float, 1, BWD>(c, s, n);
+  const int V = vec_ok(c, 2, 8) ? 8 : vec_ok(c, 2, 2) ? 2 : 1;
   if (c.dtype == GDN_DTYPE_BF16)
-    return v ? launch<__nv_bfloat16, 8, BWD>(c, s, n) : launch<__nv_bfloat16, 1, BWD>(c, s, n);
-  return v ? launch<__half, 8, BWD>(c, s, n) : launch<__half, 1, BWD>(c, s, n);
+    return V == 8   ? launch<__nv_bfloat16, 8, BWD>(c, s, n)
+           : V == 2 ? launch<__nv_bfloat16, 2, BWD>(c, s, n)
+                    : launch<__nv_bfloat16, 1, BWD>(c, s, n);
+  return V == 8 ? launch<__half, 8, BWD>(c, s, n) : V == 2 ? launch<__half, 2, BWD>(c, s, n) : launch<__half, 1, BWD>(c, s, n);
 }
 
 }  // namespace

@@ -5,16 +5,17 @@
 //   dA_log = A sum_t delta q,  dDskip = sum_t dy x,  ddt_bias = sum_t ddt.
 // The states come from the forward's every-16th-token copies: a warp goes through 16 tokens forwards with
 // their states and decays left in registers (4 states to a lane, so 128 of them), then back, so each
-// exponential is computed once.  The working warps take the registers that the feeding warps give up.
+// exponential is computed once, as a polynomial whatever the tensors' type: dA_log and the initial state's gradient
+// are fp32, and the hardware exponential's bias showed in them (against 64 bits 1.7e-6 and 2.1e-6; so 9.7e-7 and
+// 4.2e-7, for 450 us instead of 404).  The working warps take the registers that the feeding warps give up.
 // dB and dC are sums over a warp's channels for each token and state: the lanes of neighbouring channels hold
 // their four states in different orders (xor by the channel's low bits), so that what a lane keeps of a sum
 // and what it hands over are always the same registers and a butterfly step is a shuffle and an addition.
 // The feeding warps add the block's warps in shared memory, and the blocks of a group's channels leave
 // partial rows that a second kernel adds in order.  Nothing is atomic.
-// Measured at 2 x 4096 x 2048 x 16 bf16: 404 us in four segments a sequence (82 us for the first pass over them,
-// 20 for the second kernel); 569 us uncut.  Bound by shared memory (65%) and instruction issue (44%, 92 for a
-// token and scheduler) with eight working warps a multiprocessor: the sums over a warp's channels are a third of
-// the instructions.  With 184 and 176 registers instead of 192 for the working warps 407 and 457 us.
+// Measured at 2 x 4096 x 2048 x 16 bf16: 450 us in four segments a sequence (82 us for the first pass over them,
+// 20 for the second kernel).  Bound by shared memory and instruction issue (about 110 for a token and scheduler) with eight working warps a multiprocessor: the sums over a warp's channels are a third of
+// the instructions.  With 184 and 176 registers instead of 192 for the working warps it is 1% and 13% slower.
 #include <algorithm>
 #include <type_traits>
 
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int t = 4 * q + 2 * k;
-              const float2 e = decays<T>(__fmul2_rn(d2[k], {A2[j], A2[j]})), u = __fmul2_rn(__fmul2_rn(d2[k], x2[k]), b2[k]);
+              const float2 e = ex2_exact(__fmul2_rn(d2[k], {A2[j], A2[j]})), u = __fmul2_rn(__fmul2_rn(d2[k], x2[k]), b2[k]);
               a[t][j] = e.x;
               a[t + 1][j] = e.y;
               h[t][j] = fmaf(a[t][j], t > 0 ? h[t > 0 ? t - 1 : 0][j] : h0[j], u.x);
