@@ -80,8 +80,8 @@ struct Ssm {
   int N, G, dtype;
   int lg;    // log2 of a segment's tokens, in the direction that runs
   bool cut;  // whether a sequence may have several segments
-  bool vec;     // whether the per-channel tensors take 16-byte accesses
-  bool vec_bc;  // whether B and C do
+  // accesses that the per-channel tensors, and B and C, take: 2 of 16 bytes, 1 of 4, 0 of single elements
+  int vec, vec_bc;
   const void* x;
   const void* dt;
   const float* A_log;

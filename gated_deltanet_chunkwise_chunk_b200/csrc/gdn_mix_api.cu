@@ -152,19 +152,25 @@ Ssm ssm_of(const gdn_ssm_dims* d, const Seqs& s, const SsmPlan& p, void* ws, int
   return c;
 }
 
-// 16-byte accesses of x, dt, y (dy, dx, ddt): rows, their strides and a group's channels are multiples.
-bool ssm_vec(const Ssm& c) {
-  const int V = (int)(16 / esize(c.dtype));
-  if ((c.D / c.G) % V || c.ld_x % V || c.ld_dt % V) return false;
+// Accesses of x, dt, y (dy, dx, ddt): of 16 (or 4) bytes where rows, their strides and a group's channels are multiples.
+int ssm_vec(const Ssm& c) {
   const void* ps[] = {c.x, c.dt, c.y, c.dy, c.dx, c.ddt};
-  return !any_misaligned(ps, 16);
+  for (int mode = 2; mode > 0; --mode) {
+    const size_t b = mode == 2 ? 16 : 4;
+    const int64_t V = (int64_t)(b / esize(c.dtype));
+    if ((c.D / c.G) % V == 0 && c.ld_x % V == 0 && c.ld_dt % V == 0 && !any_misaligned(ps, b)) return mode;
+  }
+  return 0;
 }
 // and of B and C
-bool ssm_vec_bc(const Ssm& c) {
-  const int V = (int)(16 / esize(c.dtype));
-  if (c.N % V || c.ld_b % V || c.ld_c % V) return false;
+int ssm_vec_bc(const Ssm& c) {
   const void* ps[] = {c.Bm, c.Cm};
-  return !any_misaligned(ps, 16);
+  for (int mode = 2; mode > 0; --mode) {
+    const size_t b = mode == 2 ? 16 : 4;
+    const int64_t V = (int64_t)(b / esize(c.dtype));
+    if (c.N % V == 0 && c.ld_b % V == 0 && c.ld_c % V == 0 && !any_misaligned(ps, b)) return mode;
+  }
+  return 0;
 }
 
 // ------------------------------------------------------------------------------ norm

@@ -7,15 +7,15 @@
 // their states and decays left in registers (4 states to a lane, so 128 of them), then back, so each
 // exponential is computed once, as a polynomial whatever the tensors' type: dA_log and the initial state's gradient
 // are fp32, and the hardware exponential's bias showed in them (against 64 bits 1.7e-6 and 2.1e-6; so 9.7e-7 and
-// 4.2e-7, for 450 us instead of 404).  The working warps take the registers that the feeding warps give up.
+// 4.2e-7, for a tenth more time).  The working warps take the registers that the feeding warps give up.
 // dB and dC are sums over a warp's channels for each token and state: the lanes of neighbouring channels hold
 // their four states in different orders (xor by the channel's low bits), so that what a lane keeps of a sum
 // and what it hands over are always the same registers and a butterfly step is a shuffle and an addition.
 // The feeding warps add the block's warps in shared memory, and the blocks of a group's channels leave
 // partial rows that a second kernel adds in order.  Nothing is atomic.
-// Measured at 2 x 4096 x 2048 x 16 bf16: 450 us in four segments a sequence (82 us for the first pass over them,
+// Measured at 2 x 4096 x 2048 x 16 bf16: 442 us in four segments a sequence (82 us for the first pass over them,
 // 20 for the second kernel).  Bound by shared memory and instruction issue (about 110 for a token and scheduler) with eight working warps a multiprocessor: the sums over a warp's channels are a third of
-// the instructions.  With 184 and 176 registers instead of 192 for the working warps it is 1% and 13% slower.
+// the instructions.  With 192 and 184 registers instead of 200 for the working warps it is 2% and 10% slower.
 #include <algorithm>
 #include <type_traits>
 
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
   const int tiles = (p.len + kTile - 1) / kTile;
 
   if (at.feeds) {
-    if (!END) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (!END) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     const Inputs<T, NP, SPL> in(s, at);
     float bias[FC];
 #pragma unroll
@@ -80,12 +80,12 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
     auto fetch = [&](int i, int r) {
       if (i < tiles) {
         const int t0 = (tiles - 1 - i) * kTile, n = p.len - t0;
-        in.dt.fetch(m.rt.v[r], at.f, t0, n);
-        in.dy.fetch(m.rg.v[r], at.f, t0, n);
-        in.C.fetch(m.rc[r], at.f, t0, n);
+        in.dt.template fetch<END>(m.rt.v[r], at.f, t0, n);
+        in.dy.template fetch<END>(m.rg.v[r], at.f, t0, n);
+        in.C.template fetch<END>(m.rc[r], at.f, t0, n);
         if constexpr (!END) {
-          in.x.fetch(m.rx.v[r], at.f, t0, n);
-          in.B.fetch(m.rb[r], at.f, t0, n);
+          in.x.template fetch<END>(m.rx.v[r], at.f, t0, n);
+          in.B.template fetch<END>(m.rb[r], at.f, t0, n);
         }
       }
       copy_commit();
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
     return;
   }
 
-  if (!END) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+  if (!END) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
   // register j of a lane belongs to state n0 + (j ^ pm)
   const int pm = CW >= 4 ? at.cl & 3 : at.cl & 1;
   float A2[SPL], ga[SPL];
@@ -435,7 +435,7 @@ cudaError_t backward(const Ssm& c, cudaStream_t s) {
     ProfScope ps("ssm_bwd", s);
     constexpr size_t bytes = sizeof(BwdShared<T, NP, false>);
     if (cudaError_t e = allow_shared(k_ssm_bwd<T, NP, false>, bytes)) return e;
-    // the working warps' 192 registers and the feeding warps' 64 are the launch's 128 a thread, no more
+    // the working warps' 200 registers and the feeding warps' 56 are the launch's 128 a thread, no more
     cudaFuncAttributes f;
     if (cudaError_t e = cudaFuncGetAttributes(&f, k_ssm_bwd<T, NP, false>)) return e;
     if (f.numRegs != 128) return cudaErrorInvalidConfiguration;

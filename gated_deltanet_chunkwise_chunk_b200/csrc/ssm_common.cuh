@@ -137,18 +137,60 @@ __device__ __forceinline__ int lane_slot(int l) {
   return at;
 }
 
+// A feeding thread's share of a tile where rows do not come in 16-byte words: 4 bytes at a time (every fp32 tensor,
+// and with WORDS the even widths of the others), or half words through registers, all of a thread's loads under way
+// before the first is stored.
+template <typename T, int WIDTH, int PITCH, bool WORDS>
+__device__ __forceinline__ void fetch_narrow(T* dst, int f, const T* base, int64_t ld, int tokens, int width, int vec) {
+  if (sizeof(T) == 4 || (WORDS && vec == 1)) {
+    constexpr int V = 4 / (int)sizeof(T), PER = WIDTH / V;
+#pragma unroll(WORDS ? 4 : 1)
+    for (int i = 0; i < kTile * PER / kFeed; ++i) {
+      const int e = i * kFeed + f, t = e / PER, c = e % PER * V;
+      const bool in = t < tokens && c < width;
+      const T* src = in ? base + t * ld + c : base;
+      const unsigned d = (unsigned)__cvta_generic_to_shared(dst + t * PITCH + c);
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(in ? 4 : 0));
+    }
+  } else {
+    constexpr int ALL = kTile * WIDTH / kFeed, B = WORDS || ALL < 4 ? ALL : 4;
+#pragma unroll 1
+    for (int i0 = 0; i0 < ALL; i0 += B) {
+      T v[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int e = (i0 + i) * kFeed + f, t = e / WIDTH, c = e % WIDTH;
+        v[i] = down<T>(0.f);
+        if (t < tokens && c < width) v[i] = base[t * ld + c];
+      }
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int e = (i0 + i) * kFeed + f;
+        dst[e / WIDTH * PITCH + e % WIDTH] = v[i];
+      }
+    }
+  }
+}
+
+// The same as a call, so that the usual path keeps its registers; not for warps that have given registers up, of
+// which a called function does not know.
+template <typename T, int WIDTH, int PITCH>
+__device__ __noinline__ void fetch_narrow_call(T* dst, int f, const T* base, int64_t ld, int tokens, int width, int vec) {
+  fetch_narrow<T, WIDTH, PITCH, true>(dst, f, base, ld, tokens, width, vec);
+}
+
 // A feeding thread's share of the asynchronous copies of a [kTile][WIDTH] tile of rows with a token stride, to rows
-// of PITCH elements.  Rows of whole 16-byte words; anything else goes through registers.  What does not exist is zero.
+// of PITCH elements.  What does not exist is zero.
 template <typename T, int WIDTH, int PITCH>
 struct Feed {
   static constexpr int V = 16 / (int)sizeof(T), PER = WIDTH / V, ALL = kTile * PER, N = (ALL + kFeed - 1) / kFeed;
   const T* base;
   int64_t ld;
-  int width;
-  bool vec;
+  int width, vec;
 
+  template <bool CALL = true>
   __device__ __forceinline__ void fetch(T* dst, int f, int64_t t0, int tokens) const {
-    if (vec) {
+    if (vec == 2) {
       const int c = f % PER * V;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -159,29 +201,10 @@ struct Feed {
         const unsigned d = (unsigned)__cvta_generic_to_shared(dst + t * PITCH + c);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(in ? 16 : 0));
       }
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int i = 0; i < kTile * WIDTH / kFeed; ++i) {
-        const int e = i * kFeed + f, t = e / WIDTH, c = e % WIDTH;
-        const bool in = t < tokens && c < width;
-        const T* src = in ? base + (t0 + t) * ld + c : base;
-        const unsigned d = (unsigned)__cvta_generic_to_shared(dst + t * PITCH + c);
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(in ? 4 : 0));
-      }
-    } else {  // half words have no asynchronous copy: all of a thread's loads are under way before the first is stored
-      constexpr int PER = kTile * WIDTH / kFeed;
-      T v[PER];
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int e = i * kFeed + f, t = e / WIDTH, c = e % WIDTH;
-        v[i] = down<T>(0.f);
-        if (t < tokens && c < width) v[i] = base[(t0 + t) * ld + c];
-      }
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int e = i * kFeed + f;
-        dst[e / WIDTH * PITCH + e % WIDTH] = v[i];
-      }
+    } else if constexpr (CALL) {
+      fetch_narrow_call<T, WIDTH, PITCH>(dst, f, base + t0 * ld, ld, tokens, width, vec);
+    } else {
+      fetch_narrow<T, WIDTH, PITCH, false>(dst, f, base + t0 * ld, ld, tokens, width, vec);
     }
   }
 };
@@ -221,12 +244,16 @@ struct Cols {
       r[i / V].set_pair(i % V / 2, f);
     }
   }
-  // n: how many of them exist (vec: whole vectors of them)
-  __device__ __forceinline__ void store(T* p, bool vec, int n) const {
-    if (vec) {
+  // n: how many of them exist (whole accesses of them)
+  __device__ __forceinline__ void store(T* p, int vec, int n) const {
+    if (vec == 2) {
 #pragma unroll
       for (int i = 0; i < CW / V; ++i)
         if (i * V < n) r[i].store(p + i * V);
+    } else if (sizeof(T) == 2 && V > 1 && vec == 1) {
+#pragma unroll
+      for (int i = 0; i < CW; i += 2)
+        if (i < n) *reinterpret_cast<unsigned*>(p + i) = r[i / V].u[i % V / 2];
     } else {
 #pragma unroll
       for (int i = 0; i < CW; ++i)
