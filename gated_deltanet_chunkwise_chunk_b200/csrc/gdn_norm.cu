@@ -4,8 +4,8 @@
 //   dx = rstd (u - mean(u) - xh mean(u xh))   (rms: without mean(u)),
 //   dw = sum over rows of dn xh,  db = sum over rows of dn.
 // Bound by HBM: a row stays in registers between its statistics and its output, so x (z, dy) is read
-// once and y (dx, dz) written once.  A row belongs to a group of 1 to 32 lanes (up to 512 elements,
-// several rows to a block) or to a block of up to 512 threads; each thread holds NV vectors of it.  The variance
+// once and y (dx, dz) written once.  A row belongs to a group of 1 to 32 lanes (several rows to a
+// block) or to a block of up to 512 threads; each thread holds NV vectors of it.  The variance
 // is the mean of (x - mu)^2 over the registers, not a difference of sums.  The backward's blocks walk
 // over many rows with the weight's and bias's sums in registers and the next rows' loads in flight;
 // their partial rows are added in block order by a second kernel, so the sums do not depend on timing.
@@ -22,11 +22,6 @@ namespace mix {
 namespace {
 
 constexpr int NG = 256;  // threads of a block of lane groups
-
-template <int N>
-struct Vec {
-  float v[N];
-};
 
 // Sum of N values over the row's threads, the same result in each: lanes of the group by butterflies,
 // then the block's warps through shared memory in warp order.

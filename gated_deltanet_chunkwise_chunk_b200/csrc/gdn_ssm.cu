@@ -22,7 +22,7 @@ struct FwdShared {
 };
 
 // Measured (bf16, N = 16): 1 x 32768 x 4096 1.43 ms, with one block on each of 128 multiprocessors, bound by the
-// latency of its four working warps (issue 42%, shared memory 56%, exponentials 40% of their peaks); 8 x 1024 x 4096
+// latency of its four working warps (issue 42%, shared memory 54%, exponentials 39% of their peaks); 8 x 1024 x 4096
 // 246 us, where shared memory binds (87%: a 16-byte load is four wavefronts however many lanes want the same
 // words, 10 bytes a state and token).  The bytes alone would take 123 and 31 us, the exponentials 0.55 ms and 0.14.
 // Tried and slower: two states a lane (1.58 ms), the sums over lanes left to the feeding warps (1.54 ms), two

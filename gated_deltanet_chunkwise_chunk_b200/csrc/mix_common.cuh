@@ -76,7 +76,6 @@ struct Pack {
   };
   __device__ __forceinline__ Pack() {}
   __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const W*>(p); }
-  __device__ __forceinline__ void load_once(const T* p) { w = __ldcs(reinterpret_cast<const W*>(p)); }
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < (WORDS > 0 ? WORDS : 1); ++i) u[i] = 0u;
