@@ -61,17 +61,17 @@ def _tokens(name, t, dtype, shape, dev, lead):
         if size != 1 and stride != width:
             raise ValueError(f"{name}: the row of a token is not contiguous (strides {t.stride()})")
         width *= size
-    ld = 0
+    ld = None  # 0 is a stride too: that of a broadcast axis
     count = 1
     for size, stride in zip(reversed(t.shape[:lead]), reversed(t.stride()[:lead])):
         if size == 1:
             continue
-        if ld == 0:
+        if ld is None:
             ld = stride
         elif stride != ld * count:
             raise ValueError(f"{name}: tokens are not evenly spaced (strides {t.stride()})")
         count *= size
-    if count == 1:
+    if ld is None:
         return width
     if ld < width:
         raise ValueError(f"{name}: tokens overlap (strides {t.stride()})")

@@ -204,3 +204,22 @@ def test_backward_tensors():
 def test_norm_tensors(kw, word):
     with pytest.raises(ValueError, match=word):
         gdn.layer_norm_fwd(**{**dict(x=_z(3, 8)), **kw})
+
+
+@pytest.mark.parametrize("shape", [(2, 1, 8), (1, 3, 8)])
+def test_tokens_that_share_memory(shape):
+    """A per-token tensor broadcast along one of its two token axes has too few rows in memory for the kernels."""
+    x, w = _z(2, 3, 8), _z(8, 4, dtype=F)
+    wide = _z(*shape).expand(2, 3, 8)
+    with pytest.raises(ValueError, match="x: tokens"):
+        gdn.causal_conv_fwd(wide, w)
+    with pytest.raises(ValueError, match="x: tokens"):
+        gdn.causal_conv_bwd(wide, w, x)
+    mat = _z(2, 3, 1, 4)
+    thin = _z(*shape[:2], 1, 4).expand(2, 3, 1, 4)
+    for name, bad in (("x", (wide, x, w, mat, mat)), ("dt", (x, wide, w, mat, mat)), ("Bm", (x, x, w, thin, mat)),
+                      ("Cm", (x, x, w, mat, thin))):
+        with pytest.raises(ValueError, match=f"{name}: tokens"):
+            gdn.ssm_scan_fwd(*bad)
+    with pytest.raises(ValueError, match="x: rows"):
+        gdn.layer_norm_fwd(wide)
