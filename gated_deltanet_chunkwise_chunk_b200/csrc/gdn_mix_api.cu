@@ -38,6 +38,24 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
 }
 size_t extent(int64_t rows, int64_t ld, int64_t width, size_t es) { return rows ? ((rows - 1) * ld + width) * es : 0; }
 
+// A buffer of a call.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+// Whether an output shares bytes with an input or with another output (the workspace counts as one).
+template <size_t O, size_t I>
+bool clash(const Span (&outs)[O], const Span (&ins)[I]) {
+  for (size_t o = 0; o < O; ++o) {
+    for (const Span& i : ins)
+      if (overlap(outs[o].p, outs[o].bytes, i.p, i.bytes)) return true;
+    for (size_t q = 0; q < o; ++q)
+      if (overlap(outs[o].p, outs[o].bytes, outs[q].p, outs[q].bytes)) return true;
+  }
+  return false;
+}
+size_t cu_bytes(int64_t n) { return (size_t)(n + 1) * sizeof(int64_t); }
+
 bool workspace_ok(const void* ws, size_t have, size_t need) { return ws && !misaligned(ws, kAlign) && have >= need; }
 
 // B sequences of T tokens, or N packed into T tokens (varlen)
@@ -225,9 +243,11 @@ int gdn_conv_fwd(const gdn_conv_dims* d, const void* x, const float* weight, con
   const void* ps[] = {weight, bias, cu_seqlens, initial_state, y, final_state};
   if (any_misaligned(ps, 16)) return GDN_ERR_INVALID_ARG;
   Conv c = conv_of(d, sequences(d->B, d->T, d->N, cu_seqlens, varlen, workspace));
-  if (overlap(initial_state, st, final_state, st) || overlap(x, extent(R, c.ld, d->D, es), y, (size_t)R * d->D * es))
-    return GDN_ERR_INVALID_ARG;
-  if (!workspace_ok(workspace, workspace_bytes, conv_bytes(d, varlen, 0))) return GDN_ERR_WORKSPACE;
+  const size_t need = conv_bytes(d, varlen, 0), par = (size_t)d->D * sizeof(float);
+  const Span outs[] = {{y, (size_t)R * d->D * es}, {final_state, st}, {workspace, need}};
+  const Span ins[] = {{x, extent(R, c.ld, d->D, es)}, {weight, par * d->W}, {bias, par}, {cu_seqlens, cu_bytes(n)}, {initial_state, st}};
+  if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
+  if (!workspace_ok(workspace, workspace_bytes, need)) return GDN_ERR_WORKSPACE;
   c.x = x;
   c.weight = weight;
   c.bias = bias;
@@ -252,10 +272,12 @@ int gdn_conv_bwd(const gdn_conv_dims* d, const void* x, const float* weight, con
   const void* ps[] = {weight, bias, cu_seqlens, initial_state, dy, dfinal_state, dx, dweight, dbias, dinitial_state};
   if (any_misaligned(ps, 16)) return GDN_ERR_INVALID_ARG;
   Conv c = conv_of(d, sequences(d->B, d->T, d->N, cu_seqlens, varlen, workspace));
-  if (overlap(x, extent(R, c.ld, d->D, es), dx, rows) || overlap(dy, rows, dx, rows) || overlap(initial_state, st, dinitial_state, st) ||
-      overlap(dfinal_state, st, dinitial_state, st))
-    return GDN_ERR_INVALID_ARG;
-  if (!workspace_ok(workspace, workspace_bytes, conv_bytes(d, varlen, 1))) return GDN_ERR_WORKSPACE;
+  const size_t need = conv_bytes(d, varlen, 1), par = (size_t)d->D * sizeof(float);
+  const Span outs[] = {{dx, rows}, {dweight, par * d->W}, {dbias, par}, {dinitial_state, st}, {workspace, need}};
+  const Span ins[] = {{x, extent(R, c.ld, d->D, es)}, {weight, par * d->W}, {bias, par}, {cu_seqlens, cu_bytes(n)}, {initial_state, st},
+                      {dy, rows}, {dfinal_state, st}};
+  if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
+  if (!workspace_ok(workspace, workspace_bytes, need)) return GDN_ERR_WORKSPACE;
   c.x = x;
   c.weight = weight;
   c.bias = bias;
@@ -284,9 +306,10 @@ int gdn_conv_step(const gdn_conv_dims* d, const void* x, const float* weight, co
   if (any_misaligned(ps, 16)) return GDN_ERR_INVALID_ARG;
   if (d->B * d->D / 256 >= kMaxGrid) return GDN_ERR_INVALID_ARG;
   Conv c = conv_of(d, sequences(d->B, 1, 0, nullptr, false, nullptr));
-  if ((state != final_state && overlap(state, st, final_state, st)) ||
-      overlap(x, extent(d->B, c.ld, d->D, es), y, (size_t)d->B * d->D * es))
-    return GDN_ERR_INVALID_ARG;
+  const size_t par = (size_t)d->D * sizeof(float);
+  const Span outs[] = {{y, (size_t)d->B * d->D * es}, {final_state, st}};
+  const Span ins[] = {{x, extent(d->B, c.ld, d->D, es)}, {weight, par * d->W}, {bias, par}, {state, state == final_state ? 0 : st}};
+  if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
   c.x = x;
   c.weight = weight;
   c.bias = bias;
@@ -317,11 +340,13 @@ int gdn_ssm_fwd(const gdn_ssm_dims* d, const void* x, const void* dt, const floa
   const SsmPlan p = ssm_plan(d, varlen);
   if (!workspace_ok(workspace, workspace_bytes, p.fwd)) return GDN_ERR_WORKSPACE;
   Ssm c = ssm_of(d, sequences(d->B, d->T, d->N, cu_seqlens, varlen, workspace), p, workspace, 0);
-  const size_t rows = (size_t)R * d->D * es;
-  if (overlap(initial_state, st, final_state, st) || overlap(x, extent(R, c.ld_x, d->D, es), y, rows) ||
-      overlap(dt, extent(R, c.ld_dt, d->D, es), y, rows) || overlap(Bm, extent(R, c.ld_b, d->G * d->S, es), y, rows) ||
-      overlap(Cm, extent(R, c.ld_c, d->G * d->S, es), y, rows))
-    return GDN_ERR_INVALID_ARG;
+  const size_t par = (size_t)d->D * sizeof(float);
+  const bool keeps = workspace_bytes >= p.total;  // the states for the backward
+  const Span outs[] = {{y, (size_t)R * d->D * es}, {final_state, st}, {workspace, keeps ? p.total : p.fwd}};
+  const Span ins[] = {{x, extent(R, c.ld_x, d->D, es)}, {dt, extent(R, c.ld_dt, d->D, es)}, {A_log, par * d->S},
+                      {Bm, extent(R, c.ld_b, d->G * d->S, es)}, {Cm, extent(R, c.ld_c, d->G * d->S, es)}, {D_skip, par}, {dt_bias, par},
+                      {cu_seqlens, cu_bytes(n)}, {initial_state, st}};
+  if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
   c.x = x;
   c.dt = dt;
   c.A_log = A_log;
@@ -332,7 +357,7 @@ int gdn_ssm_fwd(const gdn_ssm_dims* d, const void* x, const void* dt, const floa
   c.init = initial_state;
   c.y = y;
   c.final = final_state;
-  if (workspace_bytes < p.total) c.ckpt = nullptr;
+  if (!keeps) c.ckpt = nullptr;
   c.vec = ssm_vec(c);
   c.vec_bc = ssm_vec_bc(c);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -357,19 +382,13 @@ int gdn_ssm_bwd(const gdn_ssm_dims* d, const void* x, const void* dt, const floa
   const SsmPlan p = ssm_plan(d, varlen);
   if (!workspace_ok(workspace, workspace_bytes, p.total)) return GDN_ERR_WORKSPACE;
   Ssm c = ssm_of(d, sequences(d->B, d->T, d->N, cu_seqlens, varlen, workspace), p, workspace, 1);
-  const size_t rows = (size_t)R * d->D * es, mats = (size_t)R * d->G * d->S * es;
-  const void* outs[] = {dx, ddt, dB, dC};
-  const size_t outn[] = {rows, rows, mats, mats};
-  const void* ins[] = {x, dt, Bm, Cm, dy};
-  const size_t inn[] = {extent(R, c.ld_x, d->D, es), extent(R, c.ld_dt, d->D, es), extent(R, c.ld_b, d->G * d->S, es),
-                        extent(R, c.ld_c, d->G * d->S, es), rows};
-  for (int o = 0; o < 4; ++o) {
-    for (int i = 0; i < 5; ++i)
-      if (overlap(ins[i], inn[i], outs[o], outn[o])) return GDN_ERR_INVALID_ARG;
-    for (int q = 0; q < o; ++q)
-      if (overlap(outs[q], outn[q], outs[o], outn[o])) return GDN_ERR_INVALID_ARG;
-  }
-  if (overlap(dfinal_state, st, dinitial_state, st)) return GDN_ERR_INVALID_ARG;
+  const size_t rows = (size_t)R * d->D * es, mats = (size_t)R * d->G * d->S * es, par = (size_t)d->D * sizeof(float);
+  const Span outs[] = {{dx, rows}, {ddt, rows}, {dB, mats}, {dC, mats}, {dA_log, par * d->S}, {dD_skip, par}, {ddt_bias, par},
+                       {dinitial_state, st}, {workspace, p.total}};
+  const Span ins[] = {{x, extent(R, c.ld_x, d->D, es)}, {dt, extent(R, c.ld_dt, d->D, es)}, {A_log, par * d->S},
+                      {Bm, extent(R, c.ld_b, d->G * d->S, es)}, {Cm, extent(R, c.ld_c, d->G * d->S, es)}, {D_skip, par}, {dt_bias, par},
+                      {cu_seqlens, cu_bytes(n)}, {dy, rows}, {dfinal_state, st}};
+  if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
   c.x = x;
   c.dt = dt;
   c.A_log = A_log;
@@ -407,10 +426,12 @@ int gdn_ssm_step(const gdn_ssm_dims* d, const void* x, const void* dt, const flo
   const void* ps[] = {A_log, D_skip, dt_bias, state, y, final_state};
   if (any_misaligned(el, es) || any_misaligned(ps, 16)) return GDN_ERR_INVALID_ARG;
   Ssm c = ssm_of(d, sequences(d->B, 1, 0, nullptr, false, nullptr), SsmPlan{}, nullptr, 0);
-  const size_t rows = (size_t)d->B * d->D * es;
-  if ((state != final_state && overlap(state, st, final_state, st)) || overlap(x, extent(d->B, c.ld_x, d->D, es), y, rows) ||
-      overlap(dt, extent(d->B, c.ld_dt, d->D, es), y, rows))
-    return GDN_ERR_INVALID_ARG;
+  const size_t par = (size_t)d->D * sizeof(float);
+  const Span outs[] = {{y, (size_t)d->B * d->D * es}, {final_state, st}};
+  const Span ins[] = {{x, extent(d->B, c.ld_x, d->D, es)}, {dt, extent(d->B, c.ld_dt, d->D, es)}, {A_log, par * d->S},
+                      {Bm, extent(d->B, c.ld_b, d->G * d->S, es)}, {Cm, extent(d->B, c.ld_c, d->G * d->S, es)}, {D_skip, par},
+                      {dt_bias, par}, {state, state == final_state ? 0 : st}};
+  if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
   c.x = x;
   c.dt = dt;
   c.A_log = A_log;
@@ -442,10 +463,11 @@ int gdn_norm_fwd(const gdn_norm_dims* d, const void* x, const float* weight, con
   const void* ps[] = {weight, bias, y, stats};
   if (any_misaligned(el, es) || any_misaligned(ps, 16)) return GDN_ERR_INVALID_ARG;
   Norm c = norm_of(d);
-  const size_t rows = (size_t)d->rows * d->D * es;
-  if (overlap(x, norm_extent(c.rows, c.inner_x, c.ld_x, c.D, es), y, rows) ||
-      overlap(gate, norm_extent(c.rows, c.inner_z, c.ld_z, c.D, es), y, rows))
-    return GDN_ERR_INVALID_ARG;
+  const size_t par = (size_t)d->D * sizeof(float);
+  const Span outs[] = {{y, (size_t)d->rows * d->D * es}, {stats, (size_t)d->rows * 2 * sizeof(float)}};
+  const Span ins[] = {{x, norm_extent(c.rows, c.inner_x, c.ld_x, c.D, es)}, {gate, norm_extent(c.rows, c.inner_z, c.ld_z, c.D, es)},
+                      {weight, par}, {bias, par}};
+  if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
   c.x = x;
   c.weight = weight;
   c.bias = bias;
@@ -466,13 +488,13 @@ int gdn_norm_bwd(const gdn_norm_dims* d, const void* x, const float* weight, con
   const void* ps[] = {weight, bias, stats, dy, dx, dgate, dweight, dbias};
   if (any_misaligned(el, es) || any_misaligned(ps, 16)) return GDN_ERR_INVALID_ARG;
   Norm c = norm_of(d);
-  const size_t rows = (size_t)d->rows * d->D * es, xe = norm_extent(c.rows, c.inner_x, c.ld_x, c.D, es),
-               ze = norm_extent(c.rows, c.inner_z, c.ld_z, c.D, es);
-  if (overlap(x, xe, dx, rows) || overlap(gate, ze, dx, rows) || overlap(dy, rows, dx, rows) || overlap(x, xe, dgate, rows) ||
-      overlap(gate, ze, dgate, rows) || overlap(dy, rows, dgate, rows) || overlap(dx, rows, dgate, rows))
-    return GDN_ERR_INVALID_ARG;
   const bool sums = dweight || dbias;
-  if (sums && !workspace_ok(workspace, workspace_bytes, gdn_norm_workspace_bytes(d))) return GDN_ERR_WORKSPACE;
+  const size_t rows = (size_t)d->rows * d->D * es, par = (size_t)d->D * sizeof(float), need = sums ? gdn_norm_workspace_bytes(d) : 0;
+  const Span outs[] = {{dx, rows}, {dgate, rows}, {dweight, par}, {dbias, par}, {workspace, need}};
+  const Span ins[] = {{x, norm_extent(c.rows, c.inner_x, c.ld_x, c.D, es)}, {gate, norm_extent(c.rows, c.inner_z, c.ld_z, c.D, es)},
+                      {weight, par}, {bias, par}, {stats, (size_t)d->rows * 2 * sizeof(float)}, {dy, rows}};
+  if (clash(outs, ins)) return GDN_ERR_INVALID_ARG;
+  if (sums && !workspace_ok(workspace, workspace_bytes, need)) return GDN_ERR_WORKSPACE;
   c.x = x;
   c.weight = weight;
   c.bias = bias;

@@ -279,8 +279,9 @@ int gdn_state_affine(int64_t count, int64_t K, int64_t V, const float* A, int tr
  * multiples of 16 bytes move in 16-byte accesses).  All other buffers are contiguous with 16-byte
  * aligned bases.  dtype: fp32, bf16 or fp16 for every per-token tensor of a call (and the
  * convolution's states); parameters, scan states and parameter gradients are fp32; all arithmetic
- * and all sums are fp32 and deterministic (no atomics).  Outputs must not overlap inputs
- * (GDN_ERR_INVALID_ARG), except a step's final_state, which may be its state.
+ * and all sums are fp32 and deterministic (no atomics).  Outputs and the workspace must
+ * not overlap inputs, parameters among them, or one another (GDN_ERR_INVALID_ARG); only a step's
+ * final_state may be its state.
  * Varlen as above: cu_seqlens packs N sequences into batch row 0, B = 1, cu[N] = T; empty sequences
  * pass their state through.  Invalid values set the workspace's status word and nothing is written.
  * Limits (GDN_ERR_INVALID_ARG): B T <= 2^30 tokens, widths <= 2^20. */

@@ -223,3 +223,34 @@ def test_tokens_that_share_memory(shape):
             gdn.ssm_scan_fwd(*bad)
     with pytest.raises(ValueError, match="x: rows"):
         gdn.layer_norm_fwd(wide)
+
+
+def _call(fn, dims, names, given, swap, tail):
+    """An entry point on distinct buffers (each far longer than needed), with buffer `swap[0]` at `swap[1]`'s address."""
+    place = {n: at(100 + i) for i, n in enumerate(given)}
+    place[swap[0]] = place[swap[1]]
+    return getattr(lib, fn)(ctypes.byref(dims), *(place.get(n) for n in names), *tail)
+
+
+OVERLAPS = [  # entry point, sizes, arguments in order, inputs, outputs, what follows
+    ("gdn_conv_fwd", conv(B=1, N=2), "x weight bias cu init y final ws", "x weight bias cu init", "y final ws", (1 << 40, None)),
+    ("gdn_conv_bwd", conv(B=1, N=2), "x weight bias cu init dy dfinal dx dweight dbias dinit ws", "x weight bias cu init dy dfinal",
+     "dx dweight dbias dinit ws", (1 << 40, None)),
+    ("gdn_conv_step", conv(T=1), "x weight bias state y final", "x weight bias state", "y final", (None,)),
+    ("gdn_ssm_fwd", ssm(B=1, N=2), "x dt A Bm Cm D dt_bias cu init y final ws", "x dt A Bm Cm D dt_bias cu init", "y final ws", (1 << 60, None)),
+    ("gdn_ssm_bwd", ssm(B=1, N=2), "x dt A Bm Cm D dt_bias cu dy dfinal dx ddt dB dC dA dD ddt_bias dinit ws",
+     "x dt A Bm Cm D dt_bias cu dy dfinal", "dx ddt dB dC dA dD ddt_bias dinit ws", (1 << 60, None)),
+    ("gdn_ssm_step", ssm(T=1), "x dt A Bm Cm D dt_bias state y final", "x dt A Bm Cm D dt_bias state", "y final", (None,)),
+    ("gdn_norm_fwd", norm(), "x weight bias gate y stats", "x weight bias gate", "y stats", (None,)),
+    ("gdn_norm_bwd", norm(), "x weight bias gate stats dy dx dgate dweight dbias ws", "x weight bias gate stats dy",
+     "dx dgate dweight dbias ws", (1 << 40, None))]
+
+
+@pytest.mark.parametrize("fn,dims,names,ins,outs,tail", OVERLAPS, ids=[o[0] for o in OVERLAPS])
+def test_no_output_overlaps_another_buffer(fn, dims, names, ins, outs, tail):
+    names, ins, outs = names.split(), ins.split(), outs.split()
+    for o in outs:
+        for other in ins + outs:
+            if other == o or (o, other) == ("final", "state"):
+                continue
+            assert _call(fn, dims, names, ins + outs, (o, other), tail) == INVALID, (o, other)
