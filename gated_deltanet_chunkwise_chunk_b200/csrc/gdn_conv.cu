@@ -39,9 +39,10 @@ cudaError_t check_packing(const Seqs& s, cudaStream_t stream) {
 
 // Columns x STR strands of rows; each strand in row order, the strands in a fixed tree.
 template <int STR>
-__global__ void __launch_bounds__(STR == 1 ? 256 : 32 * STR) k_column_sums(const float* __restrict__ part, int64_t n, int64_t ld,
-                                                                          int64_t width, float* __restrict__ out,
+__global__ void __launch_bounds__(STR == 1 ? 256 : 32 * STR) k_column_sums(Seqs seqs, const float* __restrict__ part, int64_t n,
+                                                                          int64_t ld, int64_t width, float* __restrict__ out,
                                                                           float* __restrict__ out2, int W, int64_t D) {
+  if (bad_call(seqs)) return;
   int64_t c;
   const float v = strand_sums<STR>(part, n, ld, width, c);
   if (c < 0) return;
@@ -53,13 +54,13 @@ __global__ void __launch_bounds__(STR == 1 ? 256 : 32 * STR) k_column_sums(const
   }
 }
 
-cudaError_t column_sums(const char* name, const float* part, int64_t n, int64_t ld, int64_t width, float* out,
+cudaError_t column_sums(const char* name, const Seqs& seqs, const float* part, int64_t n, int64_t ld, int64_t width, float* out,
                         float* out2, int W, int64_t D, cudaStream_t s) {
   ProfScope ps(name, s);
   switch (sum_strands(n)) {
-    case 1: k_column_sums<1><<<(unsigned)((width + 255) / 256), 256, 0, s>>>(part, n, ld, width, out, out2, W, D); break;
-    case 8: k_column_sums<8><<<(unsigned)((width + 31) / 32), 256, 0, s>>>(part, n, ld, width, out, out2, W, D); break;
-    default: k_column_sums<32><<<(unsigned)((width + 31) / 32), 1024, 0, s>>>(part, n, ld, width, out, out2, W, D);
+    case 1: k_column_sums<1><<<(unsigned)((width + 255) / 256), 256, 0, s>>>(seqs, part, n, ld, width, out, out2, W, D); break;
+    case 8: k_column_sums<8><<<(unsigned)((width + 31) / 32), 256, 0, s>>>(seqs, part, n, ld, width, out, out2, W, D); break;
+    default: k_column_sums<32><<<(unsigned)((width + 31) / 32), 1024, 0, s>>>(seqs, part, n, ld, width, out, out2, W, D);
   }
   return cudaGetLastError();
 }
@@ -571,8 +572,8 @@ cudaError_t conv_backward(const Conv& c, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   if (!c.part) return cudaSuccess;
-  return column_sums("conv_bwd_sums", c.part, conv_bwd_units(c.seqs, c.D), (c.W + 1) * c.D, (c.W + 1) * c.D, c.dweight,
-                     c.dbias, c.W, c.D, s);
+  return column_sums("conv_bwd_sums", c.seqs, c.part, conv_bwd_units(c.seqs, c.D), (c.W + 1) * c.D, (c.W + 1) * c.D,
+                     c.dweight, c.dbias, c.W, c.D, s);
 }
 
 cudaError_t conv_step(const Conv& c, cudaStream_t s) {

@@ -127,8 +127,9 @@ cudaError_t ssm_step(const Ssm& c, cudaStream_t s);
 inline int sum_strands(int64_t n) { return n <= 8 ? 1 : n <= 128 ? 8 : 32; }
 
 // Column sums of partial rows part[r * ld + c], r < n, in a fixed order: column j D + d of a row [W + 1][D] goes
-// to out[d W + j], the last D to out2; either may be null.
-cudaError_t column_sums(const char* name, const float* part, int64_t n, int64_t ld, int64_t width, float* out,
+// to out[d W + j], the last D to out2; either may be null.  With packed sequences nothing is written where their
+// boundaries were found invalid (and the rows never were).
+cudaError_t column_sums(const char* name, const Seqs& seqs, const float* part, int64_t n, int64_t ld, int64_t width, float* out,
                         float* out2, int W, int64_t D, cudaStream_t s);
 
 }  // namespace mix

@@ -554,7 +554,7 @@ cudaError_t norm_backward(const Norm& c, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   if (!c.dweight && !c.dbias) return cudaSuccess;
-  return column_sums("norm_bwd_sums", c.part, blocks, (c.dbias ? 2 : 1) * c.D, (c.dbias ? 2 : 1) * c.D, c.dweight, c.dbias,
+  return column_sums("norm_bwd_sums", Seqs{}, c.part, blocks, (c.dbias ? 2 : 1) * c.D, (c.dbias ? 2 : 1) * c.D, c.dweight, c.dbias,
                      1, c.D, s);
 }
 

@@ -11,6 +11,8 @@ Sums over tokens add a chain of at most `chain` terms: the strips or rows of a b
 """
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -424,6 +426,33 @@ def test_bad_packing_writes_nothing():
     assert gdn.gdn_device_status(ws) == 0
     gdn.causal_conv_fwd(x, w, workspace=ws.fill_(255))
     assert gdn.gdn_device_status(ws) == 0
+
+
+def test_bad_packing_leaves_gradients_alone():
+    """The C entry points of the backward passes with an invalid packing: the status word is set and no output changes."""
+    from gated_deltanet_chunkwise_chunk_b200 import binding
+    gdn, lib = _gdn(), binding.lib
+    gen = torch.Generator().manual_seed(0)
+    T, D, W, N = 20, 16, 4, 16
+    x, dy, w, b = _rand(gen, 1, T, D, dtype=BF), _rand(gen, 1, T, D, dtype=BF), _rand(gen, D, W), _rand(gen, D)
+    A_log, Bm, Cm = _rand(gen, D, N), _rand(gen, 1, T, 1, N, dtype=BF), _rand(gen, 1, T, 1, N, dtype=BF)
+    ptr = lambda t: t.data_ptr()  # noqa: E731
+    stream = torch.cuda.current_stream().cuda_stream
+    for cu in ([0, 9, 21], [0, 12, 9, 20], [1, 20], [0, 19], [-4, 20]):
+        bad, n = torch.tensor(cu, device="cuda"), len(cu) - 1
+        d = binding.gdn_conv_dims(1, T, D, W, n, 0, 1, 1)
+        ws = torch.full((gdn.conv_workspace_bytes(d, True, True),), 255, dtype=torch.uint8, device="cuda")
+        outs = [torch.full(s, 7.0, dtype=t, device="cuda") for s, t in (((1, T, D), BF), ((D, W), F32), ((D,), F32), ((n, W - 1, D), BF))]
+        assert lib.gdn_conv_bwd(ctypes.byref(d), ptr(x), ptr(w), ptr(b), ptr(bad), None, ptr(dy), None, *map(ptr, outs), ptr(ws), ws.numel(),
+                                stream) == 0
+        assert gdn.gdn_device_status(ws) == 1 and all((o == 7).all() for o in outs), cu
+        d = binding.gdn_ssm_dims(1, T, D, N, 1, n, 0, 0, 0, 0, 1)
+        ws = torch.full((gdn.ssm_workspace_bytes(d, True, True),), 255, dtype=torch.uint8, device="cuda")
+        outs = [torch.full(s, 7.0, dtype=t, device="cuda") for s, t in (
+            ((1, T, D), BF), ((1, T, D), BF), ((1, T, 1, N), BF), ((1, T, 1, N), BF), ((D, N), F32), ((D,), F32), ((D,), F32), ((n, D, N), F32))]
+        assert lib.gdn_ssm_bwd(ctypes.byref(d), ptr(x), ptr(x), ptr(A_log), ptr(Bm), ptr(Cm), None, None, ptr(bad), ptr(dy), None,
+                               *map(ptr, outs), ptr(ws), ws.numel(), stream) == 0
+        assert gdn.gdn_device_status(ws) == 1 and all((o == 7).all() for o in outs), cu
 
 
 class Layer:
