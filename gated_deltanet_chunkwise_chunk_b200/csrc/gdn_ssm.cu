@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(Shape<NP, kFwd>::NT, 3) k_ssm_fwd(Ssm s) {
   for (int j = 0; j < SPL; ++j) h[j] = 0.f;
   if (!END && at.live) {
     if (s.cut && p.idx > 0)
-      load_padded(s.starts + state_at<NP>(s, blockIdx.x, at.ch, at.n0), h);
+      load_states(s.starts + state_at<NP>(s, blockIdx.x, at.ch, 0), s.N, at.n0, h);  // nothing wrote the others
     else if (s.init)
       load_states(s.init + ((int64_t)p.seq * s.D + at.ch) * s.N, s.N, at.n0, h);
   }

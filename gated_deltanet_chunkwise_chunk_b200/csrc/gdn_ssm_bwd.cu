@@ -177,10 +177,10 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
     ga[j] = 0.f;
     dA[j] = {0.f, 0.f};
     row[j] = state_row<NP, SPL>(n);
-    if (!END && at.live) {
+    if (!END && at.live && n < s.N) {  // nothing wrote the others
       if (s.cut && p.pos + p.len < p.slen)
         ga[j] = s.starts[state_at<NP>(s, blockIdx.x, at.ch, n)];
-      else if (s.dfinal && n < s.N)
+      else if (s.dfinal)
         ga[j] = s.dfinal[((int64_t)p.seq * s.D + at.ch) * s.N + n];
     }
   }

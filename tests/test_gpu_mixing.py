@@ -223,6 +223,24 @@ def test_scan_cut_in_both_directions(lengths, packed, D, N, G):
         _scan_check(*_scan_case(5, lengths, packed, D, N, G, dtype), lengths)
 
 
+@pytest.mark.parametrize("lengths,packed,D,N,G", [([900], False, 8, 5, 1), ([1025, 1025], False, 6, 24, 2), ([2000, 3, 0, 1100], True, 16, 33, 1),
+                                                  ([800], True, 3, 9, 1), ([300, 300], False, 4, 3, 1)])
+def test_cut_scan_reads_only_what_it_wrote(lengths, packed, D, N, G):
+    """A workspace full of NaN bits changes nothing: sequences cut along time, with states that do not fill a lane's four."""
+    gdn = _gdn()
+    for dtype in (F32, BF):
+        c, init, dy, dfin = _scan_case(6, lengths, packed, D, N, G, dtype)
+        ins, rest = (c["x"], c["dt"], c["A_log"], c["Bm"], c["Cm"]), dict(D=c["D"], dt_bias=c["dt_bias"], cu_seqlens=c["cu_seqlens"])
+        need = gdn.ssm_workspace_bytes(gdn.ssm_dims(c["x"], c["Bm"], c["cu_seqlens"]), packed, True)
+        got = []
+        for fill in (0, 255):
+            ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+            y, fin = gdn.ssm_scan_fwd(*ins, **rest, initial_state=init, workspace=ws)
+            got.append(dict(y=y, state=fin, **gdn.ssm_scan_bwd(*ins, dy, ws, **rest, dfinal_state=dfin)))
+        for k in got[0]:
+            assert torch.isfinite(got[0][k].float()).all() and torch.equal(got[0][k], got[1][k]), k
+
+
 @pytest.mark.parametrize("dtype", [F32, BF, FP])
 @pytest.mark.parametrize("B,D,N,G,in_place", [(1, 8, 16, 1, True), (3, 33, 16, 1, False), (9, 24, 5, 2, True), (2, 40, 64, 1, True), (70, 16, 32, 4, False),
                                              (301, 2048, 16, 1, True), (130, 4096, 8, 2, False), (90, 4100, 12, 1, True)])
