@@ -56,20 +56,25 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // 2^t for t <= 0 of two values on the multiply-add pipe: t = n + f, f in [-1/2, 1/2], a polynomial of degree 6 in f
-// (a least-squares fit of the relative error, 2^-28), and n added to the exponent.  0.45 half ulps on average
+// (a least-squares fit of the relative error, 2^-28), times 2^n.  0.45 half ulps on average
 // without a bias, where the hardware's exponential is off by up to 2 ulp and to one side: a state that remembers a
-// thousand tokens multiplies a thousand of them.  Below 2^-126 it stays there.
+// thousand tokens multiplies a thousand of them.  Below 2^-126 it stays there.  A NaN stays a NaN: the maximum keeps it,
+// and 2^n is a factor (an integer added to the exponent would make a number of a NaN's bits).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float2 ex2_exact(float2 t) {
-  t = {fmaxf(t.x, -126.f), fmaxf(t.y, -126.f)};
-  const float2 big = {12582912.f, 12582912.f}, m = __fadd2_rn(t, big);
-  const float2 f = __fadd2_rn(t, __fmul2_rn(__fadd2_rn(m, {-12582912.f, -12582912.f}), {-1.f, -1.f}));
+  t = {max_nan(t.x, -126.f), max_nan(t.y, -126.f)};
+  constexpr float big = 12583039.f;  // 1.5 2^23 + 127: the low bits of m are n + 127, the exponent of 2^n
+  const float2 m = __fadd2_rn(t, {big, big}), f = __ffma2_rn(__fadd2_rn(m, {-big, -big}), {-1.f, -1.f}, t);
   constexpr float c[7] = {1.f,           0.693147182f,  0.240226477f,   0.0555033237f,
                           0.00961843692f, 0.00133988739f, 0.00015353362f};
   float2 p = {c[6], c[6]};
 #pragma unroll
   for (int k = 5; k >= 0; --k) p = __ffma2_rn(p, f, {c[k], c[k]});
-  return {__int_as_float(__float_as_int(p.x) + (__float_as_int(m.x) << 23)),
-          __int_as_float(__float_as_int(p.y) + (__float_as_int(m.y) << 23))};
+  return __fmul2_rn(p, {__int_as_float(__float_as_int(m.x) << 23), __int_as_float(__float_as_int(m.y) << 23)});
 }
 
 // The decays exp(delta A) of two tokens on the way forward.  Tensors of 16 bits take the hardware's exponential: its

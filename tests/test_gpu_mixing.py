@@ -281,6 +281,55 @@ def test_scan_extremes():
     assert torch.isfinite(y).all() and torch.isfinite(fin).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF, FP])
+@pytest.mark.parametrize("lengths,D", [([50, 30], 16), ([900, 40], 8), ([33, 0], 40)])
+def test_scan_of_nan_rates(lengths, D, dtype):
+    """A NaN in A_log reaches all that its state enters, in both forms, and nothing else."""
+    gdn = _gdn()
+    N, ch, st = 16, 3, 5
+    c, init, dy, dfin = _scan_case(2, lengths, True, D, N, 1, dtype)
+    before = _scan_run(c, init, dy, dfin)
+    c["A_log"][ch, st] = float("nan")
+    after = _scan_run(c, init, dy, dfin)
+    rest = [d for d in range(D) if d != ch]
+    for k in ("y", "dx", "ddt"):
+        assert torch.equal(before[k][..., rest], after[k][..., rest]), k
+    assert after["y"][..., ch].isnan().all()
+    for k in ("state", "dinitial_state"):
+        wrong = after[k] != before[k]
+        assert all(after[k][s, ch, st].isnan() for s, n in enumerate(lengths) if n > 0), k
+        wrong[[s for s, n in enumerate(lengths) if n > 0], ch, st] = False
+        assert not wrong.any(), k
+    assert after["dA_log"][ch, st].isnan() and after["ddt_bias"][ch].isnan()
+    B = 3
+    c, s0, _, _ = _scan_case(2, [1] * B, False, D, N, 1, dtype)
+    ins = (c["x"][:, 0], c["dt"][:, 0], c["A_log"], c["Bm"][:, 0], c["Cm"][:, 0], s0)
+    y, fin = gdn.ssm_step(*ins, D=c["D"], dt_bias=c["dt_bias"])
+    c["A_log"][ch, st] = float("nan")
+    y2, fin2 = gdn.ssm_step(*ins, D=c["D"], dt_bias=c["dt_bias"])
+    assert y2[:, ch].isnan().all() and fin2[:, ch, st].isnan().all()
+    assert torch.equal(y[:, rest], y2[:, rest]) and torch.equal(fin[:, rest], fin2[:, rest])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, FP])
+@pytest.mark.parametrize("lengths,D,at", [([30, 50], 16, 40), ([40, 900], 8, 700), ([5, 300], 8, 20)])
+def test_scan_backward_of_nan_steps(lengths, D, at, dtype):
+    """A NaN step is in every gradient that passes back through it: dx and ddt of its sequence's earlier tokens and the
+    initial state's gradient of its channel.  Later tokens' dx, other channels and other sequences do not see it."""
+    c, init, dy, dfin = _scan_case(4, lengths, True, D, 16, 1, dtype)
+    ch, lo = 2, lengths[0]
+    before = _scan_run(c, init, dy, dfin)
+    c["dt"][0, at, ch] = float("nan")
+    after = _scan_run(c, init, dy, dfin)
+    rest = [d for d in range(D) if d != ch]
+    for k in ("dx", "ddt"):
+        assert after[k][0, lo:at + 1, ch].isnan().all(), k
+        assert torch.equal(before[k][..., rest], after[k][..., rest]) and torch.equal(before[k][0, :lo], after[k][0, :lo]), k
+    assert torch.equal(before["dx"][0, at + 1:], after["dx"][0, at + 1:])
+    g = after["dinitial_state"]
+    assert g[1, ch].isnan().all() and torch.equal(g[0], before["dinitial_state"][0]) and torch.equal(g[1, rest], before["dinitial_state"][1, rest])
+
+
 def _short_memory(T, D, dtype):
     """Inputs whose states forget within a few tokens (delta A <= -3 for every state), so that a call's last tokens
     can be computed from the few before them."""
