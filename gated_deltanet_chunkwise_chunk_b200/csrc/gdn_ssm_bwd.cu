@@ -34,7 +34,7 @@ struct BwdShared {
   static constexpr int X = 512 / NP * kRow, S = NP * kRow;
   float d[2][X], g[2][X], c[2][S];            // delta (then ddt), dy, C
   float x[2][END ? 4 : X], b[2][END ? 4 : S]; // x (then dx), B
-  float slope[2][END ? 4 : X];                // softplus'
+  float slope[2][END ? 4 : X];                // softplus', -1 past the segment's end (where a decay is 1 and A q may overflow)
   float red[2][END ? 1 : Shape<NP, kBwd>::WORK / 32][END ? 1 : kTile][END ? 4 : 2 * NP];  // a warp's dB and dC
   // targets of 16-byte copies
   alignas(16) RawRows<T, NP> rt;
@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
         if constexpr (!END) {
           m.x[buf][to + k * kRow] = xr.get(k);
           m.x[buf][to + (k + 1) * kRow] = xr.get(k + 1);
-          m.slope[buf][to + k * kRow] = here ? softplus_slope(v.x, e.x) : 0.f;
-          m.slope[buf][to + (k + 1) * kRow] = here ? softplus_slope(v.y, e.y) : 0.f;
+          m.slope[buf][to + k * kRow] = here ? softplus_slope(v.x, e.x) : -1.f;
+          m.slope[buf][to + (k + 1) * kRow] = here ? softplus_slope(v.y, e.y) : -1.f;
         }
       }
       widen_states<T, NP, SPL>(m.c[buf], m.rc[r], at.f);
@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
 #pragma unroll
             for (int k = 0; k < M; ++k) {
               const int t = 4 * q + slot + k;
-              const float dd = d[t], xx = x[t], gy = g[t];
-              const float o = fmaf(xx, du[k], kLn2 * sq[k]) * slope[t];
+              const float dd = d[t], xx = x[t], gy = g[t], sl = slope[t];
+              const float o = sl < 0.f ? 0.f : fmaf(xx, du[k], kLn2 * sq[k]) * sl;
               x[t] = fmaf(dd, du[k], skip * gy);
               d[t] = o;
               dskip = fmaf(gy, xx, dskip);
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(STR == 1 ? 256 : 32 * STR) k_ssm_par_sums(Ssm 
   const int64_t ch = c / (s.N + 2);
   const int n = (int)(c - ch * (s.N + 2));
   if (n < s.N) {
-    if (s.dA_log) s.dA_log[ch * s.N + n] = -expf(s.A_log[ch * s.N + n]) * v;
+    if (s.dA_log) s.dA_log[ch * s.N + n] = -rate_of(s.A_log[ch * s.N + n]) * v;
   } else if (n == s.N) {
     if (s.dskip) s.dskip[ch] = v;
   } else if (s.ddt_bias) {

@@ -58,7 +58,8 @@ __device__ __forceinline__ float ex2(float x) {
 // 2^t for t <= 0 of two values on the multiply-add pipe: t = n + f, f in [-1/2, 1/2], a polynomial of degree 6 in f
 // (a least-squares fit of the relative error, 2^-28), times 2^n.  0.45 half ulps on average
 // without a bias, where the hardware's exponential is off by up to 2 ulp and to one side: a state that remembers a
-// thousand tokens multiplies a thousand of them.  Below 2^-126 it stays there.  A NaN stays a NaN: the maximum keeps it,
+// thousand tokens multiplies a thousand of them.  Below 2^-126.5 it is 0, as a decay of an
+// overflown rate has to be: its product with the rate is no gradient.  A NaN stays a NaN: the maximum keeps it,
 // and 2^n is a factor (an integer added to the exponent would make a number of a NaN's bits).
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -66,7 +67,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 __device__ __forceinline__ float2 ex2_exact(float2 t) {
-  t = {max_nan(t.x, -126.f), max_nan(t.y, -126.f)};
+  t = {max_nan(t.x, -127.f), max_nan(t.y, -127.f)};
   constexpr float big = 12583039.f;  // 1.5 2^23 + 127: the low bits of m are n + 127, the exponent of 2^n
   const float2 m = __fadd2_rn(t, {big, big}), f = __ffma2_rn(__fadd2_rn(m, {-big, -big}), {-1.f, -1.f}, t);
   constexpr float c[7] = {1.f,           0.693147182f,  0.240226477f,   0.0555033237f,
@@ -356,10 +357,16 @@ __device__ __forceinline__ void store_padded(float* p, const float (&h)[SPL]) {
   v.store(p);
 }
 
-// A log2(e), kept finite so that a token of delta = 0 past the piece's end keeps the state
+// exp(A_log) and A log2(e), kept finite so that a token of delta = 0 past the piece's end keeps the state, and a decay of 0
+// has no gradient
+constexpr float kMost = 3.4e38f;
+__device__ __forceinline__ float rate_of(float A_log) {
+  const float e = expf(A_log);
+  return e > kMost ? kMost : e;  // (false for NaN)
+}
 __device__ __forceinline__ float decay_rate(float A_log) {
   const float a = -expf(A_log) * kLog2e;
-  return a < -3.4e38f ? -3.4e38f : a;
+  return a < -kMost ? -kMost : a;
 }
 
 // that of a lane's states (0 for states that do not exist: their decay is 1, their input 0)

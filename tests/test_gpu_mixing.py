@@ -330,6 +330,20 @@ def test_scan_backward_of_nan_steps(lengths, D, at, dtype):
     assert g[1, ch].isnan().all() and torch.equal(g[0], before["dinitial_state"][0]) and torch.equal(g[1, rest], before["dinitial_state"][1, rest])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF, FP])
+@pytest.mark.parametrize("lengths,D", [([50, 30], 16), ([33], 40), ([900], 8)])
+def test_scan_of_rates_past_fp32(lengths, D, dtype):
+    """exp(A_log) near and beyond the largest fp32: the state is the last input alone, and the gradients are as finite
+    as the formulas', behind a sequence's last token (segments do not end on a tile) too."""
+    c, init, dy, dfin = _scan_case(8, lengths, True, D, 16, 1, dtype)
+    c["A_log"][1] = 100.0
+    c["A_log"][2, 3:] = 88.0
+    c["A_log"][5, ::2] = 95.0
+    c["dt"].clamp_(min=-2.0)  # with the bias: steps of 1e-3 and more, whose decays are 0 at these rates
+    c["dt_bias"].clamp_(min=-4.0)
+    _scan_check(c, init, dy, 30 * dfin, lengths)
+
+
 def _short_memory(T, D, dtype):
     """Inputs whose states forget within a few tokens (delta A <= -3 for every state), so that a call's last tokens
     can be computed from the few before them."""
