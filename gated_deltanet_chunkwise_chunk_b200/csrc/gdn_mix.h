@@ -108,7 +108,7 @@ struct Ssm {
   float* ddt_bias;
   float* dinit;
   float* part_bc;   // [channel tiles of a group][tokens][G][2][NP]
-  float* part_par;  // [units][D][N + 2]
+  float* part_par;  // [units of at most 256 tokens][D][N + 2]
 };
 
 // What a call needs besides the status word; offsets are the caller's.

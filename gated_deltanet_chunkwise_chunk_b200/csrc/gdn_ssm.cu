@@ -428,7 +428,6 @@ SsmSizes ssm_sizes(const Seqs& s, int64_t tokens, int64_t D, int N, int G) {
   SsmSizes z{};
   const int NP = ssm_padded(N), CC = 512 / NP;
   const int64_t Dg = D / G, tiles = (Dg + CC - 1) / CC, length = s.cu ? tokens / s.n : s.T, blocks = tiles * G * s.n;
-  int64_t units = 0;
   for (int pass = 0; pass < 2; ++pass) {
     z.lg[pass] = 30;
     z.cut[pass] = pass == 0 ? blocks <= 100 && length >= 768 : blocks <= 200 && length >= 256;
@@ -442,11 +441,10 @@ SsmSizes ssm_sizes(const Seqs& s, int64_t tokens, int64_t D, int N, int G) {
       z.starts = std::max(z.starts, u * D * NP);
       z.sums = std::max(z.sums, u * D);
     }
-    units = u;
   }
   z.ckpt = max_units(s, kCkptLog) * D * NP;
   z.part_bc = tiles * tokens * G * 2 * NP;
-  z.part_par = units * D * (N + 2);
+  z.part_par = max_units(s, std::min(z.lg[1], kParLog)) * D * (N + 2);
   return z;
 }
 

@@ -54,17 +54,8 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
   BwdShared<T, NP, END>& m = *reinterpret_cast<BwdShared<T, NP, END>*>(raw);
   if (bad_call(s.seqs)) return;
   Place<NP, SPL> at;
-  const bool unit = at.find(s, s.lg);
+  if (!at.find(s, s.lg)) return;
   const Piece& p = at.p;
-  float* par = s.part_par + ((int64_t)blockIdx.x * s.D + at.ch) * (s.N + 2);
-  if (!unit) {  // no such segment: its sums are empty
-    if (!END && at.live) {
-      for (int j = at.n0; j < at.n0 + SPL; ++j)
-        if (j < s.N) par[j] = 0.f;
-      if (at.nl == 0) par[s.N] = par[s.N + 1] = 0.f;
-    }
-    return;
-  }
   if (END && p.idx == 0) return;  // nothing precedes
   const int tiles = (p.len + kTile - 1) / kTile;
 
@@ -188,6 +179,20 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
   const float* ck = END ? nullptr : s.ckpt + state_at<NP>(s, first_unit(s.seqs, p.seq, kCkptLog) + p.pos / kCkpt, at.ch, at.n0);
   const int slot = lane_slot<4, NL>(at.nl);
   float total = 0.f, dskip = 0.f, dbias = 0.f;
+  // The parameters' sums leave as a row for every 256 tokens (a segment of fewer), so that no running sum is longer.
+  const int lgp = min(s.lg, kParLog);
+  auto leave = [&](int64_t row, bool zero) {
+    float* par = s.part_par + (row * s.D + at.ch) * (s.N + 2);
+#pragma unroll
+    for (int j = 0; j < SPL; ++j) {
+      const int n = at.n0 + (j ^ pm);
+      if (n < s.N) par[n] = zero ? 0.f : dA[j].x + dA[j].y;
+    }
+    if (at.nl == 0) {
+      par[s.N] = zero ? 0.f : dskip;
+      par[s.N + 1] = zero ? 0.f : dbias;
+    }
+  };
   // the state that enters the 16 tokens to come, asked for 16 tokens early
   int chunk = (p.len - 1) / kCkpt;
   float ahead[SPL];
@@ -333,15 +338,19 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
       }
     }
     total += tsum;
-  }
-  __syncthreads();
-  if constexpr (!END) {
+    if (!END && (t0 & ((1 << lgp) - 1)) == 0) {  // (a segment starts on a multiple)
 #pragma unroll
-    for (int o = 1; o < NL; o <<= 1) {
-      dskip += __shfl_xor_sync(0xffffffffu, dskip, o);
-      dbias += __shfl_xor_sync(0xffffffffu, dbias, o);
+      for (int o = 1; o < NL; o <<= 1) {
+        dskip += __shfl_xor_sync(0xffffffffu, dskip, o);
+        dbias += __shfl_xor_sync(0xffffffffu, dbias, o);
+      }
+      if (at.live) leave(first_unit(s.seqs, p.seq, lgp) + ((p.pos + t0) >> lgp), false);
+      dskip = dbias = 0.f;
+#pragma unroll
+      for (int j = 0; j < SPL; ++j) dA[j] = {0.f, 0.f};
     }
   }
+  __syncthreads();
   if (!at.live) return;
   if constexpr (END) {
 #pragma unroll
@@ -351,13 +360,12 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
 #pragma unroll
     for (int j = 0; j < SPL; ++j) {
       const int n = at.n0 + (j ^ pm);
-      if (n >= s.N) continue;
-      par[n] = dA[j].x + dA[j].y;
-      if (s.dinit && p.idx == 0) s.dinit[((int64_t)p.seq * s.D + at.ch) * s.N + n] = ga[j];
+      if (n < s.N && s.dinit && p.idx == 0) s.dinit[((int64_t)p.seq * s.D + at.ch) * s.N + n] = ga[j];
     }
-    if (at.nl == 0) {
-      par[s.N] = dskip;
-      par[s.N + 1] = dbias;
+    // rows without a token: an empty sequence's, and the one that a packed sequence may have over
+    if (p.pos + p.len == p.slen) {
+      const int64_t end = first_unit(s.seqs, p.seq + 1, lgp);
+      for (int64_t row = first_unit(s.seqs, p.seq, lgp) + ((p.slen + (1 << lgp) - 1) >> lgp); row < end; ++row) leave(row, true);
     }
   }
 }
@@ -397,13 +405,13 @@ __global__ void __launch_bounds__(256) k_ssm_bc_sums(Ssm s, int NP, int64_t tile
   }
 }
 
-// The parameters' gradients: columns of [D][N + 2], summed over the units.
+// The parameters' gradients: columns of [D][N + 2], summed over the rows of at most 256 tokens.
 template <int STR>
-__global__ void __launch_bounds__(STR == 1 ? 256 : 32 * STR) k_ssm_par_sums(Ssm s, int64_t units) {
+__global__ void __launch_bounds__(STR == 1 ? 256 : 32 * STR) k_ssm_par_sums(Ssm s, int64_t rows) {
   if (bad_call(s.seqs)) return;
   const int64_t width = s.D * (s.N + 2);
   int64_t c;
-  const float v = strand_sums<STR>(s.part_par, units, width, width, c);
+  const float v = strand_sums<STR>(s.part_par, rows, width, width, c);
   if (c < 0) return;
   const int64_t ch = c / (s.N + 2);
   const int n = (int)(c - ch * (s.N + 2));
@@ -447,11 +455,11 @@ cudaError_t backward(const Ssm& c, cudaStream_t s) {
     k_ssm_bc_sums<T><<<(unsigned)std::min<int64_t>((all + 255) / 256, 148 * 32), 256, 0, s>>>(c, NP, tiles);
   }
   ProfScope ps("ssm_bwd_par", s);
-  const int64_t width = c.D * (c.N + 2);
-  switch (sum_strands(units)) {
-    case 1: k_ssm_par_sums<1><<<(unsigned)((width + 255) / 256), 256, 0, s>>>(c, units); break;
-    case 8: k_ssm_par_sums<8><<<(unsigned)((width + 31) / 32), 256, 0, s>>>(c, units); break;
-    default: k_ssm_par_sums<32><<<(unsigned)((width + 31) / 32), 1024, 0, s>>>(c, units);
+  const int64_t width = c.D * (c.N + 2), rows = max_units(c.seqs, std::min(c.lg, kParLog));
+  switch (sum_strands(rows)) {
+    case 1: k_ssm_par_sums<1><<<(unsigned)((width + 255) / 256), 256, 0, s>>>(c, rows); break;
+    case 8: k_ssm_par_sums<8><<<(unsigned)((width + 31) / 32), 256, 0, s>>>(c, rows); break;
+    default: k_ssm_par_sums<32><<<(unsigned)((width + 31) / 32), 1024, 0, s>>>(c, rows);
   }
   return cudaGetLastError();
 }

@@ -30,6 +30,7 @@ template <typename T, int NP>
 constexpr int kRing = sizeof(T) == 4 && NP == 64 ? 2 : 3;
 constexpr int kCkpt = 16;  // tokens between the states that the forward keeps for the backward
 constexpr int kCkptLog = 4;
+constexpr int kParLog = 8;  // tokens that a partial sum of the parameters' gradients has at most
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 

@@ -63,11 +63,12 @@ def conv_bwd(x, weight, bias, cu, dy, init=None, dfinal=None, silu=True):
 # ---------------------------------------------------------------------------------- scan
 
 
-def ssm(x, dt, A_log, Bm, Cm, D=None, dt_bias=None, cu=None, init=None, dy=None, dfinal=None, extra=0.0):
+def ssm(x, dt, A_log, Bm, Cm, D=None, dt_bias=None, cu=None, init=None, dy=None, dfinal=None, extra=0.0, chain=None):
     """Forward, and with dy the backward.  x, dt [R, D]; Bm, Cm [R, G, N]; states [n, D, N].  Returns (values,
     bounds): dicts of the outputs and of bounds on the error that fp32 arithmetic (fused products, an exponential
     of 2 ulp, a softplus of (|v| + 20) half ulps) makes before an output is rounded to its type.  `extra`
-    (in half ulps of the state or gradient, at every 64th token): what a join of segments adds."""
+    (in half ulps of the state or gradient, at every 64th token): what a join of segments adds.  `chain`: additions
+    that a term of a sum over all tokens goes through, one for each token where it is not given."""
     R, W = x.shape
     G, N = Bm.shape[1:]
     n = len(cu) - 1
@@ -131,16 +132,16 @@ def ssm(x, dt, A_log, Bm, Cm, D=None, dt_bias=None, cu=None, init=None, dy=None,
             ub, hb = g * d * xx, gy * hs[t]
             Eub = np.abs(d * xx) * Eg + np.abs(ub) * (ed[t][:, None] + 3 * U)
             Ehb = np.abs(gy) * Es[t] + U * np.abs(hb)
-            for r in range(G):
-                s = group == r
-                dB[t, r], dC[t, r] = ub[s].sum(0), hb[s].sum(0)
-                EdB[t, r] = Eub[s].sum(0) + L * U * np.abs(ub[s]).sum(0)
-                EdC[t, r] = Ehb[s].sum(0) + L * U * np.abs(hb[s]).sum(0)
+            over = lambda v: v.reshape(G, W // G, N).sum(1)  # noqa: E731  (a group's channels are neighbours)
+            dB[t], dC[t] = over(ub), over(hb)
+            EdB[t] = over(Eub) + L * U * over(np.abs(ub))
+            EdC[t] = over(Ehb) + L * U * over(np.abs(hb))
             dA += d * q
             SdA += np.abs(d * q)
             EdA += d * Eq + np.abs(d * q) * (ed[t][:, None] + 2 * U)
             ga[k], Ega[k] = new, Enew
-    chain = R + 64  # tokens one after another, then units and strands
+    if chain is None:
+        chain = R + 64  # tokens one after another, then units and strands
     val.update(dx=dx, ddt=ddt, dB=dB, dC=dC, dA_log=dA * A, dD=(dy * x).sum(0), ddt_bias=ddt.sum(0), dinitial_state=ga)
     err.update(dx=Edx, ddt=Eddt, dB=EdB, dC=EdC, dA_log=np.abs(A) * (EdA + chain * U * SdA) + 6 * U * np.abs(dA * A),
                dD=chain * U * np.abs(dy * x).sum(0), ddt_bias=Eddt.sum(0) + chain * U * np.abs(ddt).sum(0),

@@ -344,6 +344,24 @@ def test_scan_of_rates_past_fp32(lengths, D, dtype):
     _scan_check(c, init, dy, 30 * dfin, lengths)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF, FP])
+def test_sums_over_a_long_whole_sequence(dtype):
+    """A sequence that is not cut along time (208 blocks): the parameters' gradients over its 6000 tokens are added
+    by rows of 256 tokens: a running sum of 128 pairs, a butterfly of the lanes, then 24 rows in 8 strands (160 additions at
+    most).  The skip's terms are exact products and all equal, so that one running sum over the sequence would round the
+    same way at every token: 674 half ulps."""
+    T, D, N = 6000, 208, 2
+    c, init, dy, dfin = _scan_case(1, [T], False, D, N, D, dtype)
+    c["x"].fill_(1 + 2.0 ** -7)
+    dy.fill_(1 + 2.0 ** -7)
+    got = _scan_run(c, init, dy, dfin)
+    flat = lambda t, *s: _np(t).reshape(T, *s)  # noqa: E731
+    val, err = om.ssm(flat(c["x"], D), flat(c["dt"], D), _np(c["A_log"]), flat(c["Bm"], D, N), flat(c["Cm"], D, N), _np(c["D"]),
+                      _np(c["dt_bias"]), [0, T], _np(init), flat(dy, D), _np(dfin), chain=160)
+    for k in ("dD", "dA_log", "ddt_bias"):
+        _close(k, got[k], val[k], err[k])
+
+
 def _short_memory(T, D, dtype):
     """Inputs whose states forget within a few tokens (delta A <= -3 for every state), so that a call's last tokens
     can be computed from the few before them."""
