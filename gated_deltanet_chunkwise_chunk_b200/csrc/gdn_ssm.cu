@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(Shape<NP, kFwd>::NT, 3) k_ssm_fwd(Ssm s) {
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float2 a = decays<T>(__fmul2_rn(d2[k], {A2[j], A2[j]})), u = __fmul2_rn(u2[k], b2[k]);
+            const float2 a = decays<T>(d2[k], {A2[j], A2[j]}), u = __fmul2_rn(u2[k], b2[k]);
             float2 hh;
             hh.x = fmaf(a.x, h[j], u.x);
             hh.y = fmaf(a.y, hh.x, u.y);
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(256, 3) k_ssm_step(Ssm s) {
         }
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
-          const float2 e = decays<T>({dk * A2[j], dk * A2[j + 1]});
+          const float2 e = decays<T>({dk, dk}, {A2[j], A2[j + 1]});
           h[k][j] = fmaf(e.x, h[k][j], uk * b[j]);
           h[k][j + 1] = fmaf(e.y, h[k][j + 1], uk * b[j + 1]);
           a = fmaf(h[k][j], c[j], a);

@@ -6,8 +6,7 @@
 // The states come from the forward's every-16th-token copies: a warp goes through 16 tokens forwards with
 // their states and decays left in registers (4 states to a lane, so 128 of them), then back, so each
 // exponential is computed once, as a polynomial whatever the tensors' type: dA_log and the initial state's gradient
-// are fp32, and the hardware exponential's bias showed in them (against 64 bits 1.7e-6 and 2.1e-6; so 9.7e-7 and
-// 4.2e-7, for a tenth more time).  The working warps take the registers that the feeding warps give up.
+// are fp32, and the hardware exponential's bias showed in them (a tenth less time).  Only the first pass over segments takes the forward's decays.  The working warps take the registers that the feeding warps give up.
 // dB and dC are sums over a warp's channels for each token and state: the lanes of neighbouring channels hold
 // their four states in different orders (xor by the channel's low bits), so that what a lane keeps of a sum
 // and what it hands over are always the same registers and a butterfly step is a shuffle and an addition.
@@ -223,7 +222,7 @@ __global__ void __launch_bounds__(Shape<NP, kBwd>::NT, 2) k_ssm_bwd(Ssm s) {
             const float2 c2[2] = {{cv.x, cv.y}, {cv.z, cv.w}};
 #pragma unroll
             for (int k = 1; k >= 0; --k) {
-              const float2 e = decays<T>(__fmul2_rn(d2[k], {A2[j], A2[j]}));
+              const float2 e = decays<T>(d2[k], {A2[j], A2[j]});
               ga[j] = e.y * fmaf(c2[k].y, g2[k].y, ga[j]);
               ga[j] = e.x * fmaf(c2[k].x, g2[k].x, ga[j]);
             }
