@@ -256,6 +256,16 @@ def test_scan_step(B, D, N, G, in_place, dtype):
     _close("state", fin, val["state"], err["state"])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF, FP])
+@pytest.mark.parametrize("B,D,N,G", [(440, 2048, 4, 1), (430, 2050, 8, 2), (101, 4096, 12, 4), (61, 4096, 32, 1), (41, 4100, 64, 2)])
+def test_scan_step_of_many_requests(B, D, N, G, dtype):
+    """Enough requests for the states to travel through the threads' rings (at least sixteen for each of the grid's rows of
+    blocks), for every number of lanes to a channel."""
+    across = -(-D * max(2, 2 ** int(np.ceil(np.log2(N))) // 4) // 256)
+    assert (B + 3) // 4 >= 4 * max(1, 148 * 3 // across) and N % 4 == 0
+    test_scan_step(B, D, N, G, True, dtype)
+
+
 def test_scan_extremes():
     """Steps above 20, decays of 0 and 1 and sequences beside infinite ones."""
     c, init, dy, dfin = _scan_case(1, [50, 30], True, 16, 16, 1, F32)
