@@ -588,6 +588,23 @@ def test_bad_packing_leaves_gradients_alone():
         assert gdn.gdn_device_status(ws) == 1 and all((o == 7).all() for o in outs), cu
 
 
+def test_sums_read_only_what_their_passes_wrote():
+    """Workspaces full of NaN bits change no gradient of the convolution and of the norm, with idle units and blocks too."""
+    gdn = _gdn()
+    spaces = [torch.full((1 << 24,), fill, dtype=torch.uint8, device="cuda") for fill in (0, 255)]
+    for lengths, packed, D, W in (([2, 0, 1, 300, 5], True, 48, 4), ([33, 0, 257], True, 257, 3), ([130, 130], False, 8, 8)):
+        c, dy, dfin = _conv_case(1, lengths, packed, D, W, BF, True, True, True, 0)
+        got = [gdn.causal_conv_bwd(c["x"], c["weight"], dy, c["bias"], "silu", c["cu_seqlens"], c["initial_state"], dfin, workspace=ws.clone())
+               for ws in spaces]
+        assert all(torch.equal(got[0][k], got[1][k]) for k in got[0])
+    gen = torch.Generator().manual_seed(1)
+    for rows, D in ((1, 64), (700, 96), (3, 4096), (2, 16400), (40, 333)):
+        x, dy, w, b = _rand(gen, rows, D), _rand(gen, rows, D), _rand(gen, D), _rand(gen, D)
+        _, stats = gdn.layer_norm_fwd(x, w, b)
+        got = [gdn.layer_norm_bwd(x, dy, stats, w, b, workspace=ws.clone()) for ws in spaces]
+        assert all(torch.equal(got[0][k], got[1][k]) for k in ("dx", "dweight", "dbias"))
+
+
 class Layer:
     """[x | z] -> convolution -> dt, B, C -> scan -> norm gated by z."""
 
