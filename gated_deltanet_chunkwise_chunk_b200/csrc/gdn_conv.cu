@@ -10,8 +10,8 @@
 // order through shared memory (32 strided loads a thread cost more than the rows: 204 us instead of 68
 // forward), and packed multiply-adds.  Measured at 2 x 8192 x 4096 bf16 with four taps and the silu: forward
 // 68 us for 268 MB (4.0 TB/s), bound by latency at two blocks a multiprocessor and by the exponentials and
-// reciprocals (half their pipe); backward 139 us for 403 MB (2.9 TB/s), bound by issue (36 instructions an
-// element); 256 single tokens of 4096 channels 10 us.
+// reciprocals (half their pipe); backward 139 us for 403 MB (2.9 TB/s), bound by latency too (issue 51%, DRAM 34% of
+// their peaks with 24% of the warps; 36 instructions an element); 256 single tokens of 4096 channels 10 us.
 #include <algorithm>
 
 #include "mix_common.cuh"

@@ -11,8 +11,9 @@
 // their partial rows are added in block order by a second kernel, so the sums do not depend on timing.
 // Measured (bf16): rows of 4096, 8192 of them, with weight and bias: forward 36 us for 134 MB (3.7 TB/s), backward
 // 59 us for 201 MB (3.4 TB/s); gated rms rows of 128, 262144 of them: forward 47 us for 201 MB (4.3 TB/s), backward
-// 95 us for 335 MB (3.5 TB/s).  What remains is issue and latency: a row's sums cost its threads as much as eight
-// elements, so a thread has 16 to 32 of them, which leaves eight to sixteen warps a multiprocessor.
+// 95 us for 335 MB (3.5 TB/s).  The forward of the heads is bound by issue (81% of its peak; DRAM 47%); the others wait
+// for their own latencies (issue 58 to 71%, DRAM 32 to 39%): a row's sums cost its threads as much as eight elements, so
+// a thread has 16 to 32 of them, which leaves sixteen warps a multiprocessor.
 #include <algorithm>
 
 #include "mix_common.cuh"

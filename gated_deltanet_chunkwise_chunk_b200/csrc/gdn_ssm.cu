@@ -22,9 +22,10 @@ struct FwdShared {
 };
 
 // Measured (bf16, N = 16): 1 x 32768 x 4096 1.43 ms, with one block on each of 128 multiprocessors, bound by the
-// latency of its four working warps (issue 42%, shared memory 54%, exponentials 39% of their peaks); 8 x 1024 x 4096
-// 246 us, where shared memory binds (87%: a 16-byte load is four wavefronts however many lanes want the same
-// words, 10 bytes a state and token).  The bytes alone would take 123 and 31 us, the exponentials 0.55 ms and 0.14.
+// latency of its four working warps (issue 40%, shared memory 54%, exponentials 39% of their peaks); 8 x 1024 x 4096
+// 237 us, where shared memory binds (87%: a 16-byte load is four wavefronts however many lanes want the same
+// words, 10 bytes a state and token, eight of them B and C widened).  The bytes alone would take 123 and 31 us, the
+// exponentials 0.55 ms and 0.14.  fp32, with the polynomial: 376 us (issue and shared memory 61% each).
 // Tried and slower: two states a lane (1.58 ms), the sums over lanes left to the feeding warps (1.54 ms), two
 // channels a lane (within 15% either way).
 // One segment.  END: only the state at its end from a zero state, and the sum of its deltas (the first
@@ -220,12 +221,14 @@ __global__ void __launch_bounds__(256) k_ssm_join(Ssm s) {
 
 // One token for each sequence: a thread has four states of a channel, so a state moves as 16 bytes, and goes through
 // the sequences four at a time: its decay rates serve all of them, and its lanes of a channel share out the four
-// softplus and the four sums.  Bound by the states' traffic.  RING: the states, B and C of the next two groups of
-// four are on their way through shared memory of the thread's own (asynchronous 16- and 8-byte copies).  Without:
-// plain loads, for calls of few sequences, which gain nothing from a ring (one request x 4096 x 16: 7.6 us, with the
-// ring 9.7), and where N or the alignment of B and C does not allow the copies.  256 requests x 4096 x 16: 35 us for
-// the 141 MB that they read and write (4.0 TB/s), without the ring 46.  init and final may be one buffer: a thread
-// reads its states before it writes them, and no other touches them.
+// softplus and the four sums.  No unit is saturated with many requests (shared memory 65%, issue 58%, DRAM 40% of
+// their peaks, 31% of the warps): it is the latency of rings whose every thread copies its own B and C.  RING: the
+// states, B and C of the next two groups of four are on their way through shared memory of the thread's own
+// (asynchronous 16- and 8-byte copies).  Without: plain loads, for calls of few sequences, which gain nothing from a
+// ring (4 requests x 4096 x 16: 3.7 us, with the ring 4.0), and where N or the alignment of B and C does not allow the
+// copies.  256 requests x 4096 x 16: 28 us for the 141 MB that they read and write (5.0 TB/s), without the ring 41; 64
+// requests, below the rule's border, 10.9 without and 9.1 with it.  init and final may be one buffer: a thread reads
+// its states before it writes them, and no other touches them.
 template <typename T, int NP, bool RING>
 __global__ void __launch_bounds__(256, 3) k_ssm_step(Ssm s) {
   constexpr int NL = NP / 4, Q = 4, OWN = NL < Q ? Q / NL : 1;  // sequences whose softplus and sum a lane has
@@ -417,13 +420,22 @@ cudaError_t dispatch(const Ssm& c, bool one, cudaStream_t s) {
 
 int ssm_padded(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
 
-// Segments.  A block goes through a token in about 58 ns forward and 139 ns backward while it has a
+// Segments.  A block goes through a token in about 44 ns forward and 142 ns backward while it has a
 // multiprocessor to itself, and up to three (two) blocks share one almost for free; the first pass costs 0.8
-// (0.4) of a pass more and its two launches some 20 (15) us.  So sequences are cut where the whole ones leave
-// most of the card idle, into as many segments as make 512 blocks, of at least 128 tokens.  Measured (bf16,
-// N = 16, forward / backward, us, whole against cut): 1 x 16384 x 2048 710 against 425, 2309 against 926;
-// 1 x 8192 x 1024 357 against 141, 1082 against 269; 2 x 4096 x 2048 187 against 228, 569 against 495;
-// 4 x 4096 x 2048 280 against 388, 780 against 882; 1 x 512 x 2048 31 against 41, 75 against 58.
+// (0.2) of a pass more and the join some 20 us.  So sequences are cut where the whole ones leave
+// most of the card idle, into as many segments as make 512 blocks, of at least 128 tokens.  Measured (device time,
+// bf16, N = 16, forward / backward, us, whole against cut):
+//   blocks 32   1 x 8192 x 1024    365 against 131   1145 against 291
+//   blocks 64   1 x 16384 x 2048   726 against 467   2328 against 1063
+//   blocks 64   1 x 512 x 2048      27 against 26      78 against 52
+//   blocks 64   1 x 256 x 2048      16 against 20      44 against 38
+//   blocks 100  1 x 4096 x 3200    185 against 180    594 against 454
+//   blocks 128  2 x 4096 x 2048    186 against 221    594 against 531
+//   blocks 200  1 x 4096 x 6400    275 against 343    872 against 826
+//   blocks 256  4 x 4096 x 2048    274 against 427    870 against 979
+// The rule goes by sizes alone and is off for short sequences at the border (1 x 512 x 4096, 128 blocks: backward 80
+// against 91) and for fp32, whose first pass has the polynomial (2 x 4096 x 2048: backward 607 against 743, 1 x 4096 x
+// 3200: forward 296 against 309).
 SsmSizes ssm_sizes(const Seqs& s, int64_t tokens, int64_t D, int N, int G) {
   SsmSizes z{};
   const int NP = ssm_padded(N), CC = 512 / NP;

@@ -12,9 +12,13 @@
 // and what it hands over are always the same registers and a butterfly step is a shuffle and an addition.
 // The feeding warps add the block's warps in shared memory, and the blocks of a group's channels leave
 // partial rows that a second kernel adds in order.  Nothing is atomic.
-// Measured at 2 x 4096 x 2048 x 16 bf16: 442 us in four segments a sequence (82 us for the first pass over them,
-// 20 for the second kernel).  Bound by shared memory and instruction issue (about 110 for a token and scheduler) with eight working warps a multiprocessor: the sums over a warp's channels are a third of
-// the instructions.  With 192 and 184 registers instead of 200 for the working warps it is 2% and 10% slower.
+// Measured at 2 x 4096 x 2048 x 16 bf16, in four segments a sequence: 425 us, 80 for the first pass over them, 19 for the
+// join, 14 and 6 for the sums, 544 in all.  No unit is saturated (shared memory 59%, issue 56% of their peaks): its eight
+// working warps a multiprocessor wait for the feeding warps and for their own latencies; about 110 instructions for a
+// token and scheduler, a third of them the sums over a warp's channels.  With 192 and 184 registers instead of 200 for
+// the working warps it is 2% and 10% slower.  A block leaves 2 NP floats of dB and dC for each token and its 512 / NP
+// channels, 4 bytes a token and channel at N = 16 and 64 at N = 64: 2 x 2048 x 2048 x 64 takes 1235 us, 85 of them the
+// kernel that adds these rows (DRAM 77%), and a workspace of 0.5 GB for them.
 #include <algorithm>
 #include <type_traits>
 

@@ -284,7 +284,10 @@ int gdn_state_affine(int64_t count, int64_t K, int64_t V, const float* A, int tr
  * final_state may be its state.
  * Varlen as above: cu_seqlens packs N sequences into batch row 0, B = 1, cu[N] = T; empty sequences
  * pass their state through.  Invalid values set the workspace's status word and nothing is written.
- * Limits (GDN_ERR_INVALID_ARG): B T <= 2^30 tokens, widths <= 2^20. */
+ * Limits (GDN_ERR_INVALID_ARG): B T <= 2^30 tokens, widths <= 2^20; for the scan also at most 65535 blocks of
+ * channels, of 512 / S each (S rounded up to 8, 16, 32 or 64; a group's blocks are its own): 524280 channels
+ * of 64 states.
+ * A NaN of an input or a parameter is not lost: what the formulas carry it to is NaN. */
 
 typedef struct gdn_conv_dims {
   int64_t B, T, D, W;  /* D channels, W taps (1..8, else GDN_ERR_UNSUPPORTED) */
