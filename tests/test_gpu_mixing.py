@@ -396,6 +396,20 @@ def test_decays_of_16_bit_calls_have_little_bias(dtype):
     assert abs(off.mean()) <= 9.7e-9, off.mean()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF, FP])
+@pytest.mark.parametrize("T", [1, 33, 900])
+def test_steps_of_zero_keep_the_state(T, dtype):
+    """A step that underflows to 0 decays by exactly 1: the state's bits stay, whole or cut along time, and in single tokens."""
+    gdn = _gdn()
+    D, N = 24, 16
+    c, init, _, _ = _scan_case(3, [T], False, D, N, 1, dtype)
+    c["dt"].fill_(-1000.0)
+    y, fin = gdn.ssm_scan_fwd(**c, initial_state=init)
+    assert torch.equal(fin, init)
+    ins = (c["x"][:, 0], c["dt"][:, 0], c["A_log"], c["Bm"][:, 0], c["Cm"][:, 0], init)
+    assert torch.equal(gdn.ssm_step(*ins, D=c["D"], dt_bias=c["dt_bias"])[1], init)
+
+
 def _short_memory(T, D, dtype):
     """Inputs whose states forget within a few tokens (delta A <= -3 for every state), so that a call's last tokens
     can be computed from the few before them."""
